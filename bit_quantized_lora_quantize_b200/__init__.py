@@ -4,7 +4,8 @@ path) for NVIDIA B200 (sm_100a).
 The product is the C-ABI library ``libqlora.so`` (include/qlora.h) built from
 ``csrc/`` by ``build.py``; ``qlora`` is its thin Python binding and
 ``synthetic`` the seeded input generator used by tests and the benchmark;
-``dp`` the data-parallel gradient bucket and ``paged`` the paged AdamW of the
+``rows`` the binding of the row-wise operators around the linears (dropout,
+layer norm), ``dp`` the data-parallel gradient bucket and ``paged`` the paged AdamW of the
 adapters.
 """
 
@@ -29,4 +30,14 @@ from .qlora import (  # noqa: F401
     qlora_profile_stop,
     qlora_quantize_nf4,
     qlora_workspace_bytes,
+)
+from .rows import (  # noqa: F401
+    new_layernorm_workspace,
+    qlora_dropout_add_layernorm_bwd,
+    qlora_dropout_add_layernorm_fwd,
+    qlora_dropout_bwd,
+    qlora_dropout_fwd,
+    qlora_layernorm_bwd,
+    qlora_layernorm_fwd,
+    qlora_layernorm_workspace_bytes,
 )

@@ -1,0 +1,50 @@
+// Host side of the row-wise kernels: argument checks shared by their entry
+// points, and the dropout launch that the linear with adapter dropout uses.
+// Not part of the public header.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/qlora.h"
+#include "rows_device.cuh"
+
+namespace qlora {
+
+constexpr int64_t kMaxRowElements = int64_t(1) << 40;
+
+inline int dtype_bytes(int32_t dtype) { return dtype == QLORA_DTYPE_FP32 ? 4 : 2; }
+inline bool known_dtype(int32_t dtype) {
+  return dtype == QLORA_DTYPE_BF16 || dtype == QLORA_DTYPE_FP16 || dtype == QLORA_DTYPE_FP32;
+}
+inline bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+// Rows of whole 16-byte vectors: eight-element groups never straddle rows.
+inline bool vector_rows(const void* p, int64_t cols) { return cols % 8 == 0 && aligned_to(p, 16); }
+
+inline qlora_status check_rows(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return QLORA_ERR_INVALID_ARG;
+  if (rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31) || rows > kMaxRowElements / cols)
+    return QLORA_ERR_UNSUPPORTED;
+  return QLORA_OK;
+}
+
+// Threshold and gain of a dropout probability (0 <= p <= 1); false when p is
+// outside that range or the counter pointer is misaligned.
+inline bool make_drop_args(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, int64_t cols,
+                           DropArgs* d) {
+  if (!(p >= 0.0 && p <= 1.0) || !aligned_to(offset_dev, 8)) return false;
+  d->seed = seed;
+  d->offset = offset;
+  d->offset_dev = offset_dev;
+  d->threshold = static_cast<uint32_t>(std::nearbyint(65536.0 * p));
+  d->gain = d->threshold < 65536u ? 65536.0f / static_cast<float>(65536u - d->threshold) : 0.0f;
+  d->groups = (cols + 7) / 8;
+  return true;
+}
+
+// Y = keep * (X * gain) + residual (residual may be null).
+cudaError_t launch_dropout(int32_t dtype, const void* X, const void* residual, void* Y, int64_t rows, int64_t cols,
+                           const DropArgs& d, cudaStream_t stream);
+
+}  // namespace qlora

@@ -28,6 +28,8 @@ STATUS_NAMES = {0: "QLORA_OK", 1: "QLORA_ERR_INVALID_ARG", 2: "QLORA_ERR_ALIGNME
 # Exported symbols and their C signatures.
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_U64 = ctypes.c_uint64
+_F64 = ctypes.c_double
 _SIGS = {
     "qlora_quantize_nf4": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P]),
     "qlora_dequantize_nf4": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P]),
@@ -47,6 +49,18 @@ _SIGS = {
                                                 ctypes.c_float, _P, _P, _P]),
     "qlora_silu_gate_fwd": (ctypes.c_int, [_P, _P, _P, _I64, _P]),
     "qlora_silu_gate_bwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P]),
+    "qlora_dropout_fwd": (ctypes.c_int, [_P, _P, _P, _I64, _I64, ctypes.c_int32, _F64, _U64, _U64, _P, _P]),
+    "qlora_dropout_bwd": (ctypes.c_int, [_P, _P, _I64, _I64, ctypes.c_int32, _F64, _U64, _U64, _P, _P]),
+    "qlora_layernorm_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.c_float, _P]),
+    "qlora_layernorm_bwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, ctypes.c_int32,
+                                           ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "qlora_dropout_add_layernorm_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, ctypes.c_int32,
+                                                       ctypes.c_int32, ctypes.c_float, _F64, _U64, _U64, _P, _P]),
+    "qlora_dropout_add_layernorm_bwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64,
+                                                       ctypes.c_int32, ctypes.c_int32, _F64, _U64, _U64, _P, _P,
+                                                       ctypes.c_size_t, _P]),
+    "qlora_layernorm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "qlora_paged_malloc": (ctypes.c_void_p, [ctypes.c_size_t, ctypes.c_int, _P]),
     "qlora_paged_free": (None, [_P, ctypes.c_size_t, ctypes.c_int, _P]),
     "qlora_paged_prefetch": (ctypes.c_int, [_P, ctypes.c_size_t, ctypes.c_int32, _P]),

@@ -285,6 +285,86 @@ QLORA_API qlora_status qlora_silu_gate_bwd(const uint16_t* G, const uint16_t* U,
                                            uint16_t* dU, int64_t n, void* stream);
 
 /*
+ * Row-wise operators of the blocks around the linears.  Matrices are
+ * [rows x cols], row-major and contiguous, of one element type `dtype`;
+ * pointers need the alignment of their elements only (rows of whole 16-byte
+ * vectors take wider accesses).  Arithmetic is float32 with one rounding per
+ * output.  rows and cols are at least 1 and below 2^31, rows * cols at most
+ * 2^40 (QLORA_ERR_UNSUPPORTED).  Outputs may not alias inputs.  Glue between
+ * LoRA linears, like the SiLU gate: the pages have no counterpart.
+ */
+typedef enum { QLORA_DTYPE_BF16 = 0, QLORA_DTYPE_FP16 = 1, QLORA_DTYPE_FP32 = 2 } qlora_dtype;
+
+/*
+ * Dropout from a counter-based generator; the mask is never stored.
+ *   forward   Y  = keep * (X * c) + residual      (residual may be NULL)
+ *   backward  dX = keep * (dY * c)                (the residual's gradient is dY)
+ * Draws: Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011) with key `seed`
+ * and the 128-bit counter (n, 0), n = offset + *offset_dev + i * ceil(cols/8)
+ * + j for columns 8j..8j+7 of row i (modulo 2^64).  Element e of the eight
+ * takes bits 16e..16e+15 of the output, word 0 first.  It is dropped when
+ * that draw is below t = round(65536 p) (ties to even), and
+ * c = 65536 / (65536 - t), so the mean is kept exactly; p = 1 drops all.
+ * What is dropped contributes exactly 0, infinities and NaN included.
+ * A call uses rows * ceil(cols/8) counters: the next call's offset is at
+ * least that much further on.  The mask does not depend on dtype.
+ *   p           0 <= p <= 1, otherwise QLORA_ERR_INVALID_ARG
+ *   offset_dev  in  device counter added to offset, or NULL: lets a captured
+ *               graph draw a new mask at each replay
+ */
+QLORA_API qlora_status qlora_dropout_fwd(const void* X, const void* residual, void* Y, int64_t rows, int64_t cols,
+                                         int32_t dtype, double p, uint64_t seed, uint64_t offset,
+                                         const uint64_t* offset_dev, void* stream);
+QLORA_API qlora_status qlora_dropout_bwd(const void* dY, void* dX, int64_t rows, int64_t cols, int32_t dtype,
+                                         double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev,
+                                         void* stream);
+
+/*
+ * Layer norm of each row, and the same fused with residual dropout.
+ *   fused:  Z = residual + dropout(X), rounded to its type; otherwise Z = X
+ *   mean = sum(Z) / cols,  rstd = 1 / sqrt(sum((Z - mean)^2) / cols + eps)
+ *   Y = (Z - mean) rstd weight + bias
+ *   weight, bias  in   [cols] of type wdtype: dtype or QLORA_DTYPE_FP32
+ *                      (QLORA_ERR_UNSUPPORTED otherwise); NULL: 1 and 0
+ *   mean, rstd    out  float[rows]; either may be NULL
+ *   eps           finite, >= 0
+ * Backward for an upstream gradient dY:
+ *   g = dY weight,  h = (Z - mean) rstd
+ *   dZ' = rstd (g - sum(g) / cols - h sum(g h) / cols) [+ dZ]
+ *   dweight = sum over rows of dY h,  dbias = sum over rows of dY
+ *   dX = dZ' (layer norm alone);  dresidual = dZ', dX = dropout(dZ') (fused)
+ *   dZ              in   gradient that reaches Z past the norm, or NULL
+ *   dweight, dbias  out  float[cols], overwritten; either may be NULL
+ *   workspace       at least qlora_layernorm_workspace_bytes bytes, the first
+ *                   256 filled with zeros once before its first use (the
+ *                   first word is read by qlora_check_status); calls that may
+ *                   overlap need one each
+ * Sums over rows are taken in a fixed order for given sizes: results are
+ * bit-reproducible run to run.
+ */
+QLORA_API qlora_status qlora_layernorm_fwd(const void* X, const void* weight, const void* bias, void* Y, float* mean,
+                                           float* rstd, int64_t rows, int64_t cols, int32_t dtype, int32_t wdtype,
+                                           float eps, void* stream);
+QLORA_API qlora_status qlora_layernorm_bwd(const void* dY, const void* X, const float* mean, const float* rstd,
+                                           const void* weight, void* dX, float* dweight, float* dbias, int64_t rows,
+                                           int64_t cols, int32_t dtype, int32_t wdtype, void* workspace,
+                                           size_t ws_bytes, void* stream);
+QLORA_API qlora_status qlora_dropout_add_layernorm_fwd(const void* X, const void* residual, const void* weight,
+                                                       const void* bias, void* Z, void* Y, float* mean, float* rstd,
+                                                       int64_t rows, int64_t cols, int32_t dtype, int32_t wdtype,
+                                                       float eps, double p, uint64_t seed, uint64_t offset,
+                                                       const uint64_t* offset_dev, void* stream);
+QLORA_API qlora_status qlora_dropout_add_layernorm_bwd(const void* dY, const void* dZ, const void* Z,
+                                                       const float* mean, const float* rstd, const void* weight,
+                                                       void* dX, void* dresidual, float* dweight, float* dbias,
+                                                       int64_t rows, int64_t cols, int32_t dtype, int32_t wdtype,
+                                                       double p, uint64_t seed, uint64_t offset,
+                                                       const uint64_t* offset_dev, void* workspace, size_t ws_bytes,
+                                                       void* stream);
+/* Workspace bytes of the two backward calls (0 for an unsupported size). */
+QLORA_API size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
  * Paged optimizer for the LoRA parameters.  "3. Paged Optimizers" and "AI
  * Glossary: QLoRA", second paragraph: only the LoRA matrices are trained,
  * and their optimizer states live in NVIDIA unified memory so that they can

@@ -31,6 +31,8 @@ Parity status per function (see each module's header):
                             special cases).
   * adamw_step / adamw_run  pinned (closed forms of the first step and of a
                             constant gradient, torch.optim.AdamW in float64).
+  * dropout / layernorm     pinned (the generator's published known-answer
+                            vectors, torch float64 autograd, differences).
 """
 
 from .nf4_ref import (  # noqa: F401
@@ -48,3 +50,11 @@ from .nf4_ref import (  # noqa: F401
 )
 from .linear_ref import lora_linear_forward, lora_linear_backward  # noqa: F401
 from .adamw_ref import adamw_step, adamw_run  # noqa: F401
+from .rows_ref import (  # noqa: F401
+    philox4x32,
+    dropout_keep,
+    dropout_gain,
+    dropout,
+    layernorm,
+    layernorm_grads,
+)

@@ -1,0 +1,84 @@
+"""Host-side refusals of the row-wise operators: every invalid call returns
+its status before anything is launched (fake pointers are never read)."""
+
+import ctypes
+
+import pytest
+import torch
+
+import bit_quantized_lora_quantize_b200 as q
+from bit_quantized_lora_quantize_b200 import build as qbuild
+
+FAKE = 1 << 20
+BF16, FP16, FP32 = 0, 1, 2
+WS = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def L():
+    qbuild.build()
+    return q.lib()
+
+
+def test_dropout_validation(L):
+    def call(x=FAKE, res=None, y=FAKE, rows=4, cols=8, dt=BF16, p=0.1, dev=None):
+        return L.qlora_dropout_fwd(x, res, y, rows, cols, dt, p, 1, 2, dev, None)
+    assert call(x=None) == 1 and call(y=None) == 1
+    assert call(rows=0) == 1 and call(cols=0) == 1 and call(rows=-1) == 1
+    assert call(dt=3) == 1 and call(dt=-1) == 1
+    assert call(p=-0.01) == 1 and call(p=1.01) == 1 and call(p=float("nan")) == 1
+    assert call(x=FAKE + 1) == 2 and call(dt=FP32, y=FAKE + 2) == 2 and call(res=FAKE + 1) == 2
+    assert call(dev=FAKE + 4) == 2
+    assert call(rows=1 << 31) == 3 and call(cols=1 << 31) == 3 and call(rows=1 << 30, cols=1 << 30) == 3
+    assert L.qlora_dropout_bwd(None, FAKE, 4, 8, BF16, 0.1, 1, 2, None, None) == 1
+    assert L.qlora_dropout_bwd(FAKE, FAKE, 4, 8, BF16, 2.0, 1, 2, None, None) == 1
+
+
+def test_layernorm_validation(L):
+    def fwd(x=FAKE, w=FAKE, b=FAKE, y=FAKE, m=FAKE, rows=4, cols=8, dt=BF16, wdt=BF16, eps=1e-5):
+        return L.qlora_layernorm_fwd(x, w, b, y, m, FAKE, rows, cols, dt, wdt, ctypes.c_float(eps), None)
+    assert fwd(x=None) == 1 and fwd(y=None) == 1
+    assert fwd(rows=0) == 1 and fwd(cols=-8) == 1
+    assert fwd(dt=5) == 1 and fwd(wdt=5) == 1
+    assert fwd(wdt=FP16) == 3 and fwd(dt=FP32, wdt=BF16) == 3
+    assert fwd(eps=-1.0) == 1 and fwd(eps=float("inf")) == 1 and fwd(eps=float("nan")) == 1
+    assert fwd(x=FAKE + 1) == 2 and fwd(w=FAKE + 1) == 2 and fwd(wdt=FP32, b=FAKE + 2) == 2 and fwd(m=FAKE + 2) == 2
+    assert fwd(rows=1 << 31) == 3
+
+    def bwd(dy=FAKE, x=FAKE, m=FAKE, r=FAKE, dx=FAKE, dw=FAKE, rows=4, cols=8, ws=FAKE, nb=WS):
+        return L.qlora_layernorm_bwd(dy, x, m, r, FAKE, dx, dw, FAKE, rows, cols, BF16, BF16, ws, nb, None)
+    assert bwd(dy=None) == 1 and bwd(x=None) == 1 and bwd(m=None) == 1 and bwd(r=None) == 1 and bwd(dx=None) == 1
+    assert bwd(rows=0) == 1 and bwd(cols=1 << 31) == 3
+    assert bwd(ws=None) == 4 and bwd(nb=L.qlora_layernorm_workspace_bytes(4, 8) - 1) == 4
+    assert bwd(ws=FAKE + 8) == 2 and bwd(dw=FAKE + 2) == 2 and bwd(dy=FAKE + 1) == 2
+
+
+def test_fused_validation(L):
+    def fwd(x=FAKE, res=FAKE, z=FAKE, p=0.1, dev=None):
+        return L.qlora_dropout_add_layernorm_fwd(x, res, FAKE, FAKE, z, FAKE, FAKE, FAKE, 4, 8, BF16, BF16,
+                                                 ctypes.c_float(1e-5), p, 1, 2, dev, None)
+    assert fwd(x=None) == 1 and fwd(res=None) == 1 and fwd(z=None) == 1 and fwd(p=1.5) == 1
+    assert fwd(dev=FAKE + 1) == 2 and fwd(z=FAKE + 1) == 2 and fwd(res=FAKE + 1) == 2
+
+    def bwd(dy=FAKE, dz=None, dx=FAKE, dres=FAKE, p=0.1, dev=None, ws=FAKE, nb=WS):
+        return L.qlora_dropout_add_layernorm_bwd(dy, dz, FAKE, FAKE, FAKE, FAKE, dx, dres, FAKE, FAKE, 4, 8, BF16, BF16,
+                                                 p, 1, 2, dev, ws, nb, None)
+    assert bwd(dy=None) == 1 and bwd(dx=None) == 1 and bwd(dres=None) == 1 and bwd(p=-1.0) == 1
+    assert bwd(dz=FAKE + 1) == 2 and bwd(dev=FAKE + 4) == 2 and bwd(ws=None) == 4 and bwd(nb=16) == 4
+
+
+def test_workspace_sizes(L):
+    assert L.qlora_layernorm_workspace_bytes(0, 8) == 0 and L.qlora_layernorm_workspace_bytes(8, 0) == 0
+    assert L.qlora_layernorm_workspace_bytes(1, 8) >= 256
+    with pytest.raises(q.QloraError):
+        q.new_layernorm_workspace(0, 8, "cpu")
+
+
+def test_binding_refuses_cpu_tensors():
+    x = torch.zeros(2, 8)
+    for call in (lambda: q.qlora_dropout_fwd(x, 0.1, 1), lambda: q.qlora_dropout_bwd(x, 0.1, 1),
+                 lambda: q.qlora_layernorm_fwd(x),
+                 lambda: q.qlora_layernorm_bwd(x, x, torch.zeros(2), torch.zeros(2)),
+                 lambda: q.qlora_dropout_add_layernorm_fwd(x, x, 0.1, 1)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
