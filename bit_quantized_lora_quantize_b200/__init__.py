@@ -32,12 +32,16 @@ from .qlora import (  # noqa: F401
     qlora_workspace_bytes,
 )
 from .rows import (  # noqa: F401
+    new_dropout_workspace,
     new_layernorm_workspace,
     qlora_dropout_add_layernorm_bwd,
     qlora_dropout_add_layernorm_fwd,
     qlora_dropout_bwd,
     qlora_dropout_fwd,
+    qlora_dropout_workspace_bytes,
     qlora_layernorm_bwd,
     qlora_layernorm_fwd,
     qlora_layernorm_workspace_bytes,
+    qlora_linear_bwd_dropout,
+    qlora_linear_fwd_dropout,
 )

@@ -17,6 +17,7 @@
 #include "abi_internal.h"
 #include "kernels.h"
 #include "nf4_host.h"
+#include "rows_host.h"
 #include "tensor_map.h"
 
 namespace qlora {
@@ -226,6 +227,190 @@ bool make_map_nd(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
 
 }  // namespace qlora
 
+namespace qlora {
+namespace {
+
+// The dropped copy of X that a linear with adapter dropout keeps at the end of
+// its workspace.
+size_t masked_bytes(int64_t M, int64_t K) { return round_up(static_cast<size_t>(M) * K * 2, 256); }
+
+// keep * X: the gain goes into the LoRA scale, so that nothing is rounded.
+cudaError_t launch_masked(const uint16_t* X, uint16_t* Xm, int64_t M, int64_t K, const DropArgs& drop,
+                          cudaStream_t stream) {
+  DropArgs d = drop;
+  d.gain = 1.0f;
+  return launch_dropout(QLORA_DTYPE_BF16, X, nullptr, Xm, M, K, d, stream);
+}
+
+qlora_status adapter_drop(int64_t K, float scale, double p, uint64_t seed, uint64_t offset,
+                          const uint64_t* offset_dev, DropArgs* d) {
+  if (!(p >= 0.0 && p <= 1.0)) return QLORA_ERR_INVALID_ARG;
+  if (!make_drop_args(p, seed, offset, offset_dev, K, d)) return QLORA_ERR_ALIGNMENT;
+  return std::isfinite(scale * d->gain) ? QLORA_OK : QLORA_ERR_INVALID_ARG;
+}
+
+// The forward, with the adapter's inputs dropped when `drop` is given.
+qlora_status linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
+                        const uint8_t* absmax_q, const float* absmax_scale, int32_t code, const uint16_t* A,
+                        const uint16_t* B, int32_t r, float scale, uint16_t* Y, float* T_save, void* workspace,
+                        size_t ws_bytes, void* stream, const DropArgs* drop) {
+  if (!X || !codes || !absmax_q || !absmax_scale || !A || !B || !Y || !T_save) return QLORA_ERR_INVALID_ARG;
+  Nf4Params Pv;
+  if (!resolve_code(code, &Pv)) return QLORA_ERR_INVALID_ARG;
+  const Nf4Params* Pc = &Pv;
+  if (!std::isfinite(scale)) return QLORA_ERR_INVALID_ARG;
+  const qlora_status sh = check_linear_shape(M, K, N, r);
+  if (sh != QLORA_OK) return sh;
+  if (drop && M > kMaxRowElements / K) return QLORA_ERR_UNSUPPORTED;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || !aligned16(T_save) ||
+      (reinterpret_cast<uintptr_t>(absmax_scale) & 3u))
+    return QLORA_ERR_ALIGNMENT;
+  const WsLayout wl = ws_layout(M, K, N, r);
+  if (!workspace || ws_bytes < wl.total + (drop ? masked_bytes(M, K) : 0)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int* status = reinterpret_cast<int*>(ws);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Nf4Params& P = *Pc;
+
+  uint16_t* Tpair = reinterpret_cast<uint16_t*>(ws + wl.t_off);
+  const int r8 = rank8(r);
+  const uint16_t* Ak = A;
+  const uint16_t* Bk = B;
+  float* Tk = T_save;
+  if (r8 != r) {
+    // The adapter padded with zero columns (A) and rows (B) to r8; T comes
+    // back through a padded buffer.
+    uint16_t* Ap = reinterpret_cast<uint16_t*>(ws + wl.pa_off);
+    uint16_t* Bp = reinterpret_cast<uint16_t*>(ws + wl.pb_off);
+    cudaError_t e = launch_pad_copy(A, K, r, r, Ap, r8, r8, 2, st);
+    if (e == cudaSuccess) e = launch_pad_copy(B, r, N, N, Bp, N, N, 2, st, r8);
+    if (e != cudaSuccess) return cuda_fail(e);
+    Ak = Ap;
+    Bk = Bp;
+    Tk = reinterpret_cast<float*>(ws + wl.pt_off);
+  }
+  cudaError_t e;
+  if (drop) {
+    // Two launches: the dropped copy of X, then the GEMM whose rank units
+    // read it (T = s c (keep * X) A, the gain c in the scale).
+    uint16_t* Xm = reinterpret_cast<uint16_t*>(ws + wl.total);
+    ProfScope p0(st, "dropout", 1);
+    e = launch_masked(X, Xm, M, K, *drop, st);
+    p0.done();
+    if (e != cudaSuccess) return cuda_fail(e);
+    ProfScope p2(st, "fused_nf4_fwd", 1);
+    e = launch_fused_fwd(X, codes, absmax_q, absmax_scale, Tpair, Bk, M, K, N, r8, Y, status, P, st, Ak, Tk,
+                         scale * drop->gain, reinterpret_cast<int*>(ws + wl.cf_off), Xm);
+    p2.done();
+  } else if (small_m_rd_path(M, K, N, r)) {
+    // Three launches: T, the weight stream, Y = bf16(stream + T B).
+    ProfScope p0(st, "small_m_nf4_fwd", 3);
+    e = launch_small_m_rd(X, codes, absmax_q, absmax_scale, Ak, Bk, M, K, N, r8, scale, Y, Tk, ws + wl.sm_off, status,
+                          P, st);
+    p0.done();
+  } else if (small_m_path(M, r)) {
+    // One launch: T, its pair and Y.
+    ProfScope p0(st, "small_m_nf4_fwd", 1);
+    e = launch_small_m_fwd(X, codes, absmax_q, absmax_scale, Ak, Bk, M, K, N, r8, scale, Y, Tk, Tpair,
+                           ws + wl.sm_off, status, P, st);
+    p0.done();
+  } else {
+    // One launch: T = s X A (T_save and its pair) in the kernel's first
+    // units, then the output tiles.
+    ProfScope p2(st, "fused_nf4_fwd", 1);
+    e = launch_fused_fwd(X, codes, absmax_q, absmax_scale, Tpair, Bk, M, K, N, r8, Y, status, P, st, Ak, Tk, scale,
+                         reinterpret_cast<int*>(ws + wl.cf_off));
+    p2.done();
+  }
+  if (e == cudaSuccess && r8 != r) e = launch_pad_copy(Tk, M, r8, r8, T_save, r, r, 4, st);
+  return e == cudaSuccess ? QLORA_OK : cuda_fail(e);
+}
+
+// The backward, of the forward with dropped adapter inputs when `drop` is given.
+qlora_status linear_bwd(const uint16_t* dY, const uint16_t* X, const float* T_save, int64_t M, int64_t K, int64_t N,
+                        const uint8_t* codes, const uint8_t* absmax_q, const float* absmax_scale, int32_t code,
+                        const uint16_t* A, const uint16_t* B, int32_t r, float scale, uint16_t* dX, float* dA,
+                        float* dB, void* workspace, size_t ws_bytes, void* stream, const DropArgs* drop) {
+  if (!dY || !X || !T_save || !codes || !absmax_q || !absmax_scale || !A || !B || !dX || !dA || !dB)
+    return QLORA_ERR_INVALID_ARG;
+  Nf4Params Pv;
+  if (!resolve_code(code, &Pv)) return QLORA_ERR_INVALID_ARG;
+  const Nf4Params* Pc = &Pv;
+  if (!std::isfinite(scale)) return QLORA_ERR_INVALID_ARG;
+  const qlora_status sh = check_linear_shape(M, K, N, r);
+  if (sh != QLORA_OK) return sh;
+  if (drop && M > kMaxRowElements / K) return QLORA_ERR_UNSUPPORTED;
+  if (!aligned16(dY) || !aligned16(X) || !aligned16(T_save) || !aligned16(codes) || !aligned16(A) ||
+      !aligned16(B) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) ||
+      (reinterpret_cast<uintptr_t>(absmax_scale) & 3u))
+    return QLORA_ERR_ALIGNMENT;
+  const WsLayout wl = ws_layout(M, K, N, r);
+  if (!workspace || ws_bytes < wl.total + (drop ? masked_bytes(M, K) : 0)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int* status = reinterpret_cast<int*>(ws);
+  uint16_t* Tpair = reinterpret_cast<uint16_t*>(ws + wl.t_off);
+  uint16_t* Upair = reinterpret_cast<uint16_t*>(ws + wl.u_off);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Nf4Params& P = *Pc;
+
+  const int r8 = rank8(r);
+  const uint16_t* Ak = A;
+  const uint16_t* Bk = B;
+  const float* Tk = T_save;
+  float* dAk = dA;
+  float* dBk = dB;
+  cudaError_t e = cudaSuccess;
+  if (r8 != r) {
+    uint16_t* Ap = reinterpret_cast<uint16_t*>(ws + wl.pa_off);
+    uint16_t* Bp = reinterpret_cast<uint16_t*>(ws + wl.pb_off);
+    float* Tp = reinterpret_cast<float*>(ws + wl.pt_off);
+    e = launch_pad_copy(A, K, r, r, Ap, r8, r8, 2, st);
+    if (e == cudaSuccess) e = launch_pad_copy(B, r, N, N, Bp, N, N, 2, st, r8);
+    if (e == cudaSuccess) e = launch_pad_copy(T_save, M, r, r, Tp, r8, r8, 4, st);
+    if (e != cudaSuccess) return cuda_fail(e);
+    Ak = Ap;
+    Bk = Bp;
+    Tk = Tp;
+    dAk = reinterpret_cast<float*>(ws + wl.pda_off);
+    dBk = reinterpret_cast<float*>(ws + wl.pdb_off);
+  }
+  // One launch: U = s dY B^T (and the bf16 pair of T) in the first units,
+  // the dX tiles, and dA = X^T U and dB = T^T dY in units that fill the SMs
+  // the last wave of tiles leaves idle.
+  // With adapter dropout dA reads the dropped copy of X, drawn again, and the
+  // adapter's part of dX is added by a third launch: its mask differs per
+  // element, so it cannot share the accumulators of dY W'.
+  const uint16_t* Xa = X;
+  if (drop) {
+    uint16_t* Xm = reinterpret_cast<uint16_t*>(ws + wl.total);
+    ProfScope p0(st, "dropout", 1);
+    e = launch_masked(X, Xm, M, K, *drop, st);
+    p0.done();
+    if (e != cudaSuccess) return cuda_fail(e);
+    Xa = Xm;
+  }
+  ProfScope p2(st, "fused_nf4_dx", 1);
+  e = launch_fused_dx(dY, codes, absmax_q, absmax_scale, Upair, Ak, M, K, N, r8, dX, status, P, st, Bk,
+                      drop ? scale * drop->gain : scale, reinterpret_cast<int*>(ws + wl.cd_off), Xa, Tk, Tpair, dAk,
+                      dBk, !drop);
+  p2.done();
+  if (e == cudaSuccess && drop) {
+    ProfScope p3(st, "adapter_dx", 1);
+    e = launch_adapter_dx(Upair, Ak, dX, M, K, r8, *drop, st);
+    p3.done();
+  }
+  if (e == cudaSuccess && r8 != r) {
+    e = launch_pad_copy(dAk, K, r8, r8, dA, r, r, 4, st);
+    if (e == cudaSuccess) e = launch_pad_copy(dBk, r, N, N, dB, N, N, 4, st);
+  }
+  return e == cudaSuccess ? QLORA_OK : cuda_fail(e);
+}
+
+}  // namespace
+}  // namespace qlora
+
 using namespace qlora;
 
 extern "C" {
@@ -282,64 +467,8 @@ qlora_status qlora_linear_fwd_4bit(const uint16_t* X, int64_t M, int64_t K, int6
                                    const uint8_t* absmax_q, const float* absmax_scale, int32_t code,
                                    const uint16_t* A, const uint16_t* B, int32_t r, float scale, uint16_t* Y,
                                    float* T_save, void* workspace, size_t ws_bytes, void* stream) {
-  if (!X || !codes || !absmax_q || !absmax_scale || !A || !B || !Y || !T_save) return QLORA_ERR_INVALID_ARG;
-  Nf4Params Pv;
-  if (!resolve_code(code, &Pv)) return QLORA_ERR_INVALID_ARG;
-  const Nf4Params* Pc = &Pv;
-  if (!std::isfinite(scale)) return QLORA_ERR_INVALID_ARG;
-  const qlora_status sh = check_linear_shape(M, K, N, r);
-  if (sh != QLORA_OK) return sh;
-  if (!aligned16(X) || !aligned16(codes) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || !aligned16(T_save) ||
-      (reinterpret_cast<uintptr_t>(absmax_scale) & 3u))
-    return QLORA_ERR_ALIGNMENT;
-  const WsLayout wl = ws_layout(M, K, N, r);
-  if (!workspace || ws_bytes < wl.total) return QLORA_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  int* status = reinterpret_cast<int*>(ws);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const Nf4Params& P = *Pc;
-
-  uint16_t* Tpair = reinterpret_cast<uint16_t*>(ws + wl.t_off);
-  const int r8 = rank8(r);
-  const uint16_t* Ak = A;
-  const uint16_t* Bk = B;
-  float* Tk = T_save;
-  if (r8 != r) {
-    // The adapter padded with zero columns (A) and rows (B) to r8; T comes
-    // back through a padded buffer.
-    uint16_t* Ap = reinterpret_cast<uint16_t*>(ws + wl.pa_off);
-    uint16_t* Bp = reinterpret_cast<uint16_t*>(ws + wl.pb_off);
-    cudaError_t e = launch_pad_copy(A, K, r, r, Ap, r8, r8, 2, st);
-    if (e == cudaSuccess) e = launch_pad_copy(B, r, N, N, Bp, N, N, 2, st, r8);
-    if (e != cudaSuccess) return cuda_fail(e);
-    Ak = Ap;
-    Bk = Bp;
-    Tk = reinterpret_cast<float*>(ws + wl.pt_off);
-  }
-  cudaError_t e;
-  if (small_m_rd_path(M, K, N, r)) {
-    // Three launches: T, the weight stream, Y = bf16(stream + T B).
-    ProfScope p0(st, "small_m_nf4_fwd", 3);
-    e = launch_small_m_rd(X, codes, absmax_q, absmax_scale, Ak, Bk, M, K, N, r8, scale, Y, Tk, ws + wl.sm_off, status,
-                          P, st);
-    p0.done();
-  } else if (small_m_path(M, r)) {
-    // One launch: T, its pair and Y.
-    ProfScope p0(st, "small_m_nf4_fwd", 1);
-    e = launch_small_m_fwd(X, codes, absmax_q, absmax_scale, Ak, Bk, M, K, N, r8, scale, Y, Tk, Tpair,
-                           ws + wl.sm_off, status, P, st);
-    p0.done();
-  } else {
-    // One launch: T = s X A (T_save and its pair) in the kernel's first
-    // units, then the output tiles.
-    ProfScope p2(st, "fused_nf4_fwd", 1);
-    e = launch_fused_fwd(X, codes, absmax_q, absmax_scale, Tpair, Bk, M, K, N, r8, Y, status, P, st, Ak, Tk, scale,
-                         reinterpret_cast<int*>(ws + wl.cf_off));
-    p2.done();
-  }
-  if (e == cudaSuccess && r8 != r) e = launch_pad_copy(Tk, M, r8, r8, T_save, r, r, 4, st);
-  return e == cudaSuccess ? QLORA_OK : cuda_fail(e);
+  return linear_fwd(X, M, K, N, codes, absmax_q, absmax_scale, code, A, B, r, scale, Y, T_save, workspace, ws_bytes,
+                    stream, nullptr);
 }
 
 qlora_status qlora_linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
@@ -355,61 +484,8 @@ qlora_status qlora_linear_bwd_4bit(const uint16_t* dY, const uint16_t* X, const 
                                    const float* absmax_scale, int32_t code, const uint16_t* A, const uint16_t* B,
                                    int32_t r, float scale, uint16_t* dX, float* dA, float* dB, void* workspace,
                                    size_t ws_bytes, void* stream) {
-  if (!dY || !X || !T_save || !codes || !absmax_q || !absmax_scale || !A || !B || !dX || !dA || !dB)
-    return QLORA_ERR_INVALID_ARG;
-  Nf4Params Pv;
-  if (!resolve_code(code, &Pv)) return QLORA_ERR_INVALID_ARG;
-  const Nf4Params* Pc = &Pv;
-  if (!std::isfinite(scale)) return QLORA_ERR_INVALID_ARG;
-  const qlora_status sh = check_linear_shape(M, K, N, r);
-  if (sh != QLORA_OK) return sh;
-  if (!aligned16(dY) || !aligned16(X) || !aligned16(T_save) || !aligned16(codes) || !aligned16(A) ||
-      !aligned16(B) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) ||
-      (reinterpret_cast<uintptr_t>(absmax_scale) & 3u))
-    return QLORA_ERR_ALIGNMENT;
-  const WsLayout wl = ws_layout(M, K, N, r);
-  if (!workspace || ws_bytes < wl.total) return QLORA_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  int* status = reinterpret_cast<int*>(ws);
-  uint16_t* Tpair = reinterpret_cast<uint16_t*>(ws + wl.t_off);
-  uint16_t* Upair = reinterpret_cast<uint16_t*>(ws + wl.u_off);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const Nf4Params& P = *Pc;
-
-  const int r8 = rank8(r);
-  const uint16_t* Ak = A;
-  const uint16_t* Bk = B;
-  const float* Tk = T_save;
-  float* dAk = dA;
-  float* dBk = dB;
-  cudaError_t e = cudaSuccess;
-  if (r8 != r) {
-    uint16_t* Ap = reinterpret_cast<uint16_t*>(ws + wl.pa_off);
-    uint16_t* Bp = reinterpret_cast<uint16_t*>(ws + wl.pb_off);
-    float* Tp = reinterpret_cast<float*>(ws + wl.pt_off);
-    e = launch_pad_copy(A, K, r, r, Ap, r8, r8, 2, st);
-    if (e == cudaSuccess) e = launch_pad_copy(B, r, N, N, Bp, N, N, 2, st, r8);
-    if (e == cudaSuccess) e = launch_pad_copy(T_save, M, r, r, Tp, r8, r8, 4, st);
-    if (e != cudaSuccess) return cuda_fail(e);
-    Ak = Ap;
-    Bk = Bp;
-    Tk = Tp;
-    dAk = reinterpret_cast<float*>(ws + wl.pda_off);
-    dBk = reinterpret_cast<float*>(ws + wl.pdb_off);
-  }
-  // One launch: U = s dY B^T (and the bf16 pair of T) in the first units,
-  // the dX tiles, and dA = X^T U and dB = T^T dY in units that fill the SMs
-  // the last wave of tiles leaves idle.
-  ProfScope p2(st, "fused_nf4_dx", 1);
-  e = launch_fused_dx(dY, codes, absmax_q, absmax_scale, Upair, Ak, M, K, N, r8, dX, status, P, st, Bk, scale,
-                      reinterpret_cast<int*>(ws + wl.cd_off), X, Tk, Tpair, dAk, dBk);
-  p2.done();
-  if (e == cudaSuccess && r8 != r) {
-    e = launch_pad_copy(dAk, K, r8, r8, dA, r, r, 4, st);
-    if (e == cudaSuccess) e = launch_pad_copy(dBk, r, N, N, dB, N, N, 4, st);
-  }
-  return e == cudaSuccess ? QLORA_OK : cuda_fail(e);
+  return linear_bwd(dY, X, T_save, M, K, N, codes, absmax_q, absmax_scale, code, A, B, r, scale, dX, dA, dB, workspace,
+                    ws_bytes, stream, nullptr);
 }
 
 qlora_status qlora_linear_bwd(const uint16_t* dY, const uint16_t* X, const float* T_save, int64_t M, int64_t K,
@@ -418,6 +494,36 @@ qlora_status qlora_linear_bwd(const uint16_t* dY, const uint16_t* X, const float
                               float* dB, void* workspace, size_t ws_bytes, void* stream) {
   return qlora_linear_bwd_4bit(dY, X, T_save, M, K, N, codes, absmax_q, absmax_scale, QLORA_CODE_NF4, A, B, r, scale,
                                dX, dA, dB, workspace, ws_bytes, stream);
+}
+
+qlora_status qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
+                                      const uint8_t* absmax_q, const float* absmax_scale, int32_t code,
+                                      const uint16_t* A, const uint16_t* B, int32_t r, float scale, double p,
+                                      uint64_t seed, uint64_t offset, const uint64_t* offset_dev, uint16_t* Y,
+                                      float* T_save, void* workspace, size_t ws_bytes, void* stream) {
+  DropArgs d;
+  const qlora_status s = adapter_drop(K, scale, p, seed, offset, offset_dev, &d);
+  return s != QLORA_OK ? s
+                       : linear_fwd(X, M, K, N, codes, absmax_q, absmax_scale, code, A, B, r, scale, Y, T_save,
+                                    workspace, ws_bytes, stream, &d);
+}
+
+qlora_status qlora_linear_bwd_dropout(const uint16_t* dY, const uint16_t* X, const float* T_save, int64_t M,
+                                      int64_t K, int64_t N, const uint8_t* codes, const uint8_t* absmax_q,
+                                      const float* absmax_scale, int32_t code, const uint16_t* A, const uint16_t* B,
+                                      int32_t r, float scale, double p, uint64_t seed, uint64_t offset,
+                                      const uint64_t* offset_dev, uint16_t* dX, float* dA, float* dB,
+                                      void* workspace, size_t ws_bytes, void* stream) {
+  DropArgs d;
+  const qlora_status s = adapter_drop(K, scale, p, seed, offset, offset_dev, &d);
+  return s != QLORA_OK ? s
+                       : linear_bwd(dY, X, T_save, M, K, N, codes, absmax_q, absmax_scale, code, A, B, r, scale, dX,
+                                    dA, dB, workspace, ws_bytes, stream, &d);
+}
+
+size_t qlora_dropout_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t r) {
+  if (check_linear_shape(M, K, N, r) != QLORA_OK || M > kMaxRowElements / K) return 0;
+  return ws_layout(M, K, N, r).total + masked_bytes(M, K);
 }
 
 qlora_status qlora_silu_gate_fwd(const uint16_t* G, const uint16_t* U, uint16_t* H, int64_t n, void* stream) {

@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fused_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmC,
                       const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2,
                       const __grid_constant__ CUtensorMap tmAbs, const __grid_constant__ CUtensorMap tmR,
-                      const __grid_constant__ TailMaps tm, const PairArgs args) {
+                      const __grid_constant__ CUtensorMap tmRA, const __grid_constant__ TailMaps tm,
+                      const PairArgs args) {
   using L = PairSmem<MNB>;
   constexpr uint32_t kTmemCols = 512;  // two 128 x 256 fp32 accumulators
 
@@ -253,7 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmC);
     tma_prefetch_desc(&tmA2);
     tma_prefetch_desc(&tmB2);
-    if (args.r_units) tma_prefetch_desc(&tmR);
+    if (args.r_units) {
+      tma_prefetch_desc(&tmR);
+      tma_prefetch_desc(&tmRA);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
@@ -337,8 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i < args.nkb) {
           const int kb = i;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::kA + (runit ? 2 * args.unit_cols * kDepth * 2 : 0));
-          tma_load_2d_pair(&tmA, full_leader, a_dst, kb * kDepth, row0);
-          tma_load_2d_pair(&tmA, full_leader, a_dst + 16384, kb * kDepth, row0 + 256);
+          // Rank units may read other rows than the tiles (tmRA): the adapter's
+          // dropped inputs in a forward with adapter dropout.
+          const CUtensorMap* am = runit ? &tmRA : &tmA;
+          tma_load_2d_pair(am, full_leader, a_dst, kb * kDepth, row0);
+          tma_load_2d_pair(am, full_leader, a_dst + 16384, kb * kDepth, row0 + 256);
           if (runit) {
             // This CTA's unit_cols adapter columns (64-wide boxes): forward
             // A[K, r] rows of block kb (MN-major B operand), input gradient
@@ -754,8 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool MNB>
 cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& c, const CUtensorMap& a2, const CUtensorMap& b2,
-                        const CUtensorMap& abs, const CUtensorMap& rmap, const TailMaps& tmaps, const PairArgs& args,
-                        cudaStream_t stream) {
+                        const CUtensorMap& abs, const CUtensorMap& rmap, const CUtensorMap& ra,
+                        const TailMaps& tmaps, const PairArgs& args, cudaStream_t stream) {
   using L = PairSmem<MNB>;
   static_assert(L::kDynamic <= 232448, "shared memory budget");
   auto kern = fused_pair_kernel<MNB>;
@@ -774,7 +781,7 @@ cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& c, const CUtens
   attr[1] = pdl_attribute();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a, c, a2, b2, abs, rmap, tmaps, args);
+  return cudaLaunchKernelEx(&cfg, kern, a, c, a2, b2, abs, rmap, ra, tmaps, args);
 }
 
 // Row blocks per tile group: as few groups as keep one group's activation
@@ -819,7 +826,7 @@ int fused_ctr_ints(int64_t M) { return 2 + static_cast<int>((M + kPairRows - 1) 
 cudaError_t launch_fused_fwd(const uint16_t* X, const uint8_t* codes, const uint8_t* absmax_q,
                              const float* absmax_scale, uint16_t* Tpair, const uint16_t* B, int64_t M, int64_t K,
                              int64_t N, int r, uint16_t* Y, int* status, const Nf4Params& P, cudaStream_t stream,
-                             const uint16_t* A, float* T_save, float scale, int* ctr) {
+                             const uint16_t* A, float* T_save, float scale, int* ctr, const uint16_t* X_adapter) {
   const int rp = lora_pad(r);
   CUtensorMap mX, mC, mT, mB, mR;
   if (!make_map_2d(&mX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, K, M, K * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -836,6 +843,10 @@ cudaError_t launch_fused_fwd(const uint16_t* X, const uint8_t* codes, const uint
                      CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
+  CUtensorMap mRA = mX;
+  if (X_adapter && !make_map_2d(&mRA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X_adapter, K, M, K * 2, 64, 128,
+                                CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   PairArgs args{};
   plan_units(args, M, N, K, r, scale, ctr, T_save, Tpair);
   args.nkb = static_cast<int>(K / 64);
@@ -854,14 +865,14 @@ cudaError_t launch_fused_fwd(const uint16_t* X, const uint8_t* codes, const uint
   args.wait_ns = wait_limit_ns();
   args.nf4 = P;
   const TailMaps none{mB, mB, mB, mB};
-  return launch_pair<false>(mX, mC, mT, mB, mB, mR, none, args, stream);
+  return launch_pair<false>(mX, mC, mT, mB, mB, mR, mRA, none, args, stream);
 }
 
 cudaError_t launch_fused_dx(const uint16_t* dY, const uint8_t* codes, const uint8_t* absmax_q,
                             const float* absmax_scale, uint16_t* Upair, const uint16_t* A, int64_t M, int64_t K,
                             int64_t N, int r, uint16_t* dX, int* status, const Nf4Params& P, cudaStream_t stream,
                             const uint16_t* B, float scale, int* ctr, const uint16_t* X, const float* T_save,
-                            uint16_t* Tpair, float* dA, float* dB) {
+                            uint16_t* Tpair, float* dA, float* dB, bool lora_stages) {
   const int rp = lora_pad(r);
   CUtensorMap mD, mC, mU, mA, mR;
   if (!make_map_2d(&mD, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, N, M, N * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -908,7 +919,7 @@ cudaError_t launch_fused_dx(const uint16_t* dY, const uint8_t* codes, const uint
     args.t_pair = Tpair;
   }
   args.nkb = static_cast<int>((N + 63) / 64);
-  args.lora_kb = 2 * rp / 64;
+  args.lora_kb = lora_stages ? 2 * rp / 64 : 0;
   args.lora_mod = rp;
   args.rows = static_cast<int>(M);
   args.cols = static_cast<int>(K);
@@ -922,7 +933,7 @@ cudaError_t launch_fused_dx(const uint16_t* dY, const uint8_t* codes, const uint
   args.status = status;
   args.wait_ns = wait_limit_ns();
   args.nf4 = P;
-  return launch_pair<true>(mD, mC, mU, mA, mAbs, mR, tails, args, stream);
+  return launch_pair<true>(mD, mC, mU, mA, mAbs, mR, mD, tails, args, stream);
 }
 
 }  // namespace qlora

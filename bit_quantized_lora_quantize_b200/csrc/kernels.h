@@ -56,23 +56,25 @@ inline int lora_pad(int r) { return (r + 63) / 64 * 64; }
 // computes T = s X A itself (T_save float32 and the pair in Tpair) in units
 // that run ahead of the output tiles; with ctr == nullptr Tpair must be the
 // output of the previous kernel in the stream (A, T_save, scale unused).
+// With `X_adapter` (and `ctr`) the adapter reads these rows instead of X.
 cudaError_t launch_fused_fwd(const uint16_t* X, const uint8_t* codes, const uint8_t* absmax_q,
                              const float* absmax_scale, uint16_t* Tpair, const uint16_t* B, int64_t M, int64_t K,
                              int64_t N, int r, uint16_t* Y, int* status, const Nf4Params& P, cudaStream_t stream,
                              const uint16_t* A = nullptr, float* T_save = nullptr, float scale = 0.0f,
-                             int* ctr = nullptr);
+                             int* ctr = nullptr, const uint16_t* X_adapter = nullptr);
 
 // Fused dequant-GEMM, input gradient: dX[M,K] = dY[M,N] W'[N,K] + (U_hi + U_lo)[M,r] A[K,r]^T.
 // With `ctr` the kernel also computes U = s dY B^T (its pair in Upair) the
 // same way, and, when dA and dB are given, dA = X^T U and dB = T^T dY (the
 // rank units write the bf16 pair of T_save into Tpair for that); with
-// ctr == nullptr Upair comes from the previous kernel.
+// ctr == nullptr Upair comes from the previous kernel.  Without `lora_stages`
+// dX is dY W' alone (the caller adds the adapter's part from Upair).
 cudaError_t launch_fused_dx(const uint16_t* dY, const uint8_t* codes, const uint8_t* absmax_q,
                             const float* absmax_scale, uint16_t* Upair, const uint16_t* A, int64_t M, int64_t K,
                             int64_t N, int r, uint16_t* dX, int* status, const Nf4Params& P, cudaStream_t stream,
                             const uint16_t* B = nullptr, float scale = 0.0f, int* ctr = nullptr,
                             const uint16_t* X = nullptr, const float* T_save = nullptr, uint16_t* Tpair = nullptr,
-                            float* dA = nullptr, float* dB = nullptr);
+                            float* dA = nullptr, float* dB = nullptr, bool lora_stages = true);
 
 // Counter ints one fused launch with rank units needs for M rows.
 int fused_ctr_ints(int64_t M);

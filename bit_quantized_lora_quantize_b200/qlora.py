@@ -61,6 +61,13 @@ _SIGS = {
                                                        ctypes.c_int32, ctypes.c_int32, _F64, _U64, _U64, _P, _P,
                                                        ctypes.c_size_t, _P]),
     "qlora_layernorm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "qlora_linear_fwd_dropout": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, ctypes.c_int32, _P, _P,
+                                                ctypes.c_int32, ctypes.c_float, _F64, _U64, _U64, _P, _P, _P, _P,
+                                                ctypes.c_size_t, _P]),
+    "qlora_linear_bwd_dropout": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, ctypes.c_int32, _P, _P,
+                                                ctypes.c_int32, ctypes.c_float, _F64, _U64, _U64, _P, _P, _P, _P,
+                                                _P, ctypes.c_size_t, _P]),
+    "qlora_dropout_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, ctypes.c_int32]),
     "qlora_paged_malloc": (ctypes.c_void_p, [ctypes.c_size_t, ctypes.c_int, _P]),
     "qlora_paged_free": (None, [_P, ctypes.c_size_t, ctypes.c_int, _P]),
     "qlora_paged_prefetch": (ctypes.c_int, [_P, ctypes.c_size_t, ctypes.c_int32, _P]),

@@ -1,6 +1,6 @@
 """Thin Python binding of the row-wise operators of ``libqlora.so``: dropout
-from a counter-based generator, layer norm, and the two fused with a residual
-sum (formulas in include/qlora.h).
+from a counter-based generator, layer norm, the two fused with a residual sum,
+and the linear whose adapter sees dropped inputs (formulas in include/qlora.h).
 
 A tensor of any shape is a matrix whose rows run along its last dimension.
 Every call runs on the tensors' device, on that device's current stream.
@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from .qlora import QloraError, _check, _ptr, lib
+from .qlora import PackedNF4, QloraError, _check, _ptr, lib, packed_sizes
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -232,6 +232,87 @@ def qlora_dropout_add_layernorm_bwd(dY: torch.Tensor, dZ: torch.Tensor | None, Z
     return dX, dresidual, dweight, dbias
 
 
+# ---------------------------------------------------------------- linear with adapter dropout
+def qlora_dropout_workspace_bytes(M: int, K: int, N: int, r: int) -> int:
+    return int(lib().qlora_dropout_workspace_bytes(M, K, N, r))
+
+
+def new_dropout_workspace(M: int, K: int, N: int, r: int, device) -> torch.Tensor:
+    """Workspace of the linear calls with adapter dropout for these sizes."""
+    nbytes = qlora_dropout_workspace_bytes(M, K, N, r)
+    if nbytes == 0:
+        raise QloraError("qlora_dropout_workspace_bytes", 3, f"M={M} K={K} N={N} r={r}")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def _linear(X: torch.Tensor, W: PackedNF4, A: torch.Tensor, B: torch.Tensor, workspace: torch.Tensor | None):
+    """(M, K, N, r, workspace) of a linear call, its inputs checked."""
+    if not X.is_cuda:
+        raise ValueError("qlora kernels take CUDA tensors only (no CPU path)")
+    if X.dim() != 2 or len(W.shape) != 2 or A.dim() != 2 or B.dim() != 2:
+        raise ValueError("matrices expected")
+    (M, K), N, r = X.shape, W.shape[0], A.shape[1]
+    _typed(X, (M, K), torch.bfloat16, "X", X)
+    _typed(X, (K, r), torch.bfloat16, "A", A)
+    _typed(X, (r, N), torch.bfloat16, "B", B)
+    nc, nb, nb2 = packed_sizes(N * K)
+    _typed(X, (nc,), torch.uint8, "W.codes", W.codes)
+    _typed(X, (nb,), torch.uint8, "W.absmax_q", W.absmax_q)
+    _typed(X, (nb2 + (W.dq == "centred_fp8"),), torch.float32, "W.absmax_scale", W.absmax_scale)
+    if W.shape[1] != K:
+        raise ValueError("W: [N, K] for inputs [M, K] expected")
+    if workspace is None:
+        workspace = new_dropout_workspace(M, K, N, r, X.device)
+    _typed(X, (workspace.numel(),), torch.uint8, "workspace", workspace)
+    return M, K, N, r, workspace
+
+
+def _typed(X: torch.Tensor, shape: tuple, dtype: torch.dtype, what: str, t: torch.Tensor) -> torch.Tensor:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != X.device or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous {dtype} of shape {tuple(shape)} on {X.device} expected")
+    return t
+
+
+def _out(X: torch.Tensor, shape: tuple, dtype: torch.dtype, what: str, t: torch.Tensor | None) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=X.device) if t is None else _typed(X, shape, dtype, what, t)
+
+
+def qlora_linear_fwd_dropout(X: torch.Tensor, W: PackedNF4, A: torch.Tensor, B: torch.Tensor, scale: float, p: float,
+                             seed: int, offset: int = 0, workspace: torch.Tensor | None = None,
+                             Y: torch.Tensor | None = None, T_save: torch.Tensor | None = None,
+                             offset_dev: torch.Tensor | None = None):
+    """(Y, T_save) for Y = X W'^T + (s dropout(X) A) B; the draws are those of
+    ``qlora_dropout_fwd(X, p, seed, offset)``."""
+    M, K, N, r, workspace = _linear(X, W, A, B, workspace)
+    Y = _out(X, (M, N), torch.bfloat16, "Y", Y)
+    T_save = _out(X, (M, r), torch.float32, "T_save", T_save)
+    dev = _draws(X, seed, offset, offset_dev)
+    _call("qlora_linear_fwd_dropout", X.device, _ptr(X), M, K, N, _ptr(W.codes), _ptr(W.absmax_q),
+          _ptr(W.absmax_scale), W.code_value, _ptr(A), _ptr(B), r, scale, p, seed, offset, dev, _ptr(Y), _ptr(T_save),
+          _ptr(workspace), workspace.numel())
+    return Y, T_save
+
+
+def qlora_linear_bwd_dropout(dY: torch.Tensor, X: torch.Tensor, T_save: torch.Tensor, W: PackedNF4, A: torch.Tensor,
+                             B: torch.Tensor, scale: float, p: float, seed: int, offset: int = 0,
+                             workspace: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                             dA: torch.Tensor | None = None, dB: torch.Tensor | None = None,
+                             offset_dev: torch.Tensor | None = None):
+    """(dX, dA, dB) of the forward drawn with the same p, seed and offset."""
+    M, K, N, r, workspace = _linear(X, W, A, B, workspace)
+    _typed(X, (M, N), torch.bfloat16, "dY", dY)
+    _typed(X, (M, r), torch.float32, "T_save", T_save)
+    dX = _out(X, (M, K), torch.bfloat16, "dX", dX)
+    dA = _out(X, (K, r), torch.float32, "dA", dA)
+    dB = _out(X, (r, N), torch.float32, "dB", dB)
+    dev = _draws(X, seed, offset, offset_dev)
+    _call("qlora_linear_bwd_dropout", X.device, _ptr(dY), _ptr(X), _ptr(T_save), M, K, N, _ptr(W.codes),
+          _ptr(W.absmax_q), _ptr(W.absmax_scale), W.code_value, _ptr(A), _ptr(B), r, scale, p, seed, offset, dev,
+          _ptr(dX), _ptr(dA), _ptr(dB), _ptr(workspace), workspace.numel())
+    return dX, dA, dB
+
+
 __all__ = ["qlora_dropout_fwd", "qlora_dropout_bwd", "qlora_layernorm_workspace_bytes", "new_layernorm_workspace",
            "qlora_layernorm_fwd", "qlora_layernorm_bwd", "qlora_dropout_add_layernorm_fwd",
-           "qlora_dropout_add_layernorm_bwd"]
+           "qlora_dropout_add_layernorm_bwd", "qlora_dropout_workspace_bytes", "new_dropout_workspace",
+           "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout"]

@@ -320,6 +320,40 @@ QLORA_API qlora_status qlora_dropout_bwd(const void* dY, void* dX, int64_t rows,
                                          void* stream);
 
 /*
+ * The linear layer with dropout on the adapter's inputs (the frozen product
+ * reads X as it is):
+ *   Y  = bf16(X W'^T + T B),      T_save = s (dropout(X) A)
+ *   U  = s dY B^T,  dB = T_save^T dY,  dA = dropout(X)^T U,
+ *   dX = dY W' + keep * c (U A^T)
+ * with the draws of qlora_dropout_fwd for rows = M, cols = K; the backward
+ * takes the forward's p, seed, offset and counter and draws the mask again.
+ * The gain c is applied in float32 to the rank-r intermediates, so the
+ * dropped inputs take no rounding of their own.  dX is rounded to bf16 twice:
+ * dY W', then its sum with the adapter's part.
+ * Same supported shapes, code values, buffers and workspace rule as
+ * qlora_linear_fwd_4bit / qlora_linear_bwd_4bit, with a workspace of at least
+ * qlora_dropout_workspace_bytes bytes (it holds a dropped copy of X during a
+ * call, besides what the plain calls keep there).  Every M runs the pair
+ * GEMMs of the large-M calls.  s * c must be finite
+ * (QLORA_ERR_INVALID_ARG), M * K at most 2^40.
+ */
+QLORA_API qlora_status qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,
+                                                const uint8_t* codes, const uint8_t* absmax_q,
+                                                const float* absmax_scale, int32_t code, const uint16_t* A,
+                                                const uint16_t* B, int32_t r, float scale, double p, uint64_t seed,
+                                                uint64_t offset, const uint64_t* offset_dev, uint16_t* Y,
+                                                float* T_save, void* workspace, size_t ws_bytes, void* stream);
+QLORA_API qlora_status qlora_linear_bwd_dropout(const uint16_t* dY, const uint16_t* X, const float* T_save,
+                                                int64_t M, int64_t K, int64_t N, const uint8_t* codes,
+                                                const uint8_t* absmax_q, const float* absmax_scale, int32_t code,
+                                                const uint16_t* A, const uint16_t* B, int32_t r, float scale,
+                                                double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev,
+                                                uint16_t* dX, float* dA, float* dB, void* workspace, size_t ws_bytes,
+                                                void* stream);
+/* Workspace bytes of the two calls (0 for an unsupported shape). */
+QLORA_API size_t qlora_dropout_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t r);
+
+/*
  * Layer norm of each row, and the same fused with residual dropout.
  *   fused:  Z = residual + dropout(X), rounded to its type; otherwise Z = X
  *   mean = sum(Z) / cols,  rstd = 1 / sqrt(sum((Z - mean)^2) / cols + eps)

@@ -67,6 +67,28 @@ def test_fused_validation(L):
     assert bwd(dz=FAKE + 1) == 2 and bwd(dev=FAKE + 4) == 2 and bwd(ws=None) == 4 and bwd(nb=16) == 4
 
 
+def test_linear_dropout_validation(L):
+    need = L.qlora_dropout_workspace_bytes(16, 256, 256, 8)
+    assert need >= L.qlora_workspace_bytes(16, 256, 256, 8) + 16 * 256 * 2
+    assert L.qlora_dropout_workspace_bytes(16, 250, 256, 8) == 0
+
+    def fwd(x=FAKE, K=256, r=8, code=0, s=1.0, p=0.1, dev=None, ws=FAKE, nb=need):
+        return L.qlora_linear_fwd_dropout(x, 16, K, 256, FAKE, FAKE, FAKE, code, FAKE, FAKE, r, ctypes.c_float(s), p, 1,
+                                          2, dev, FAKE, FAKE, ws, nb, None)
+    assert fwd(x=None) == 1 and fwd(p=1.01) == 1 and fwd(p=float("nan")) == 1 and fwd(s=float("inf")) == 1
+    assert fwd(s=3e38, p=0.9) == 1  # the gain carries the scale past float32
+    assert fwd(code=9) == 1 and fwd(r=0) == 1
+    assert fwd(x=FAKE + 2) == 2 and fwd(dev=FAKE + 4) == 2
+    assert fwd(K=250) == 3 and fwd(r=257) == 3
+    assert fwd(ws=None) == 4 and fwd(nb=need - 1) == 4
+
+    def bwd(dy=FAKE, t=FAKE, s=1.0, p=0.1, dev=None, nb=need):
+        return L.qlora_linear_bwd_dropout(dy, FAKE, t, 16, 256, 256, FAKE, FAKE, FAKE, 0, FAKE, FAKE, 8,
+                                          ctypes.c_float(s), p, 1, 2, dev, FAKE, FAKE, FAKE, FAKE, nb, None)
+    assert bwd(dy=None) == 1 and bwd(t=None) == 1 and bwd(p=-0.1) == 1 and bwd(s=float("nan")) == 1
+    assert bwd(dev=FAKE + 1) == 2 and bwd(nb=need - 1) == 4
+
+
 def test_workspace_sizes(L):
     assert L.qlora_layernorm_workspace_bytes(0, 8) == 0 and L.qlora_layernorm_workspace_bytes(8, 0) == 0
     assert L.qlora_layernorm_workspace_bytes(1, 8) >= 256
