@@ -5,7 +5,7 @@ The product is the C-ABI library ``libqlora.so`` (include/qlora.h) built from
 ``csrc/`` by ``build.py``; ``qlora`` is its thin Python binding and
 ``synthetic`` the seeded input generator used by tests and the benchmark;
 ``rows`` the binding of the row-wise operators around the linears (dropout,
-layer norm), ``dp`` the data-parallel gradient bucket and ``paged`` the paged AdamW of the
+layer norm), ``int8`` that of the linear on 8-bit integer weights, ``dp`` the data-parallel gradient bucket and ``paged`` the paged AdamW of the
 adapters.
 """
 
@@ -44,4 +44,12 @@ from .rows import (  # noqa: F401
     qlora_layernorm_workspace_bytes,
     qlora_linear_bwd_dropout,
     qlora_linear_fwd_dropout,
+)
+from .int8 import (  # noqa: F401
+    PackedInt8,
+    new_int8_workspace,
+    qlora_int8_workspace_bytes,
+    qlora_linear_int8_fwd,
+    qlora_matmul_int8,
+    qlora_quantize_int8,
 )

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libqlora.so")
 SOURCES = ["abi.cu", "fused_pair.cu", "smallm.cu", "smallm_rd.cu", "quantize.cu", "nf4_host.cu", "noalloc.cu", "glue.cu", "adamw.cu",
-           "dropout.cu", "layernorm.cu", "adapter_dx.cu"]
+           "dropout.cu", "layernorm.cu", "adapter_dx.cu", "int8.cu"]
 HEADERS = ["ptx.cuh", "nf4_device.cuh", "kernels.h", "tensor_map.h", "nf4_host.h", "abi_internal.h",
            "rows_device.cuh", "rows_host.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

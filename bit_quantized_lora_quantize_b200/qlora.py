@@ -68,6 +68,12 @@ _SIGS = {
                                                 ctypes.c_int32, ctypes.c_float, _F64, _U64, _U64, _P, _P, _P, _P,
                                                 _P, ctypes.c_size_t, _P]),
     "qlora_dropout_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, ctypes.c_int32]),
+    "qlora_quantize_int8": (ctypes.c_int, [_P, _I64, _I64, ctypes.c_int32, _P, _I64, _P, _P]),
+    "qlora_matmul_int8": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _P, ctypes.c_int32, _P,
+                                         ctypes.c_size_t, _P]),
+    "qlora_linear_int8_fwd": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.c_int32, _P, _I64, _P, _P, _P,
+                                             ctypes.c_size_t, _P]),
+    "qlora_int8_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "qlora_paged_malloc": (ctypes.c_void_p, [ctypes.c_size_t, ctypes.c_int, _P]),
     "qlora_paged_free": (None, [_P, ctypes.c_size_t, ctypes.c_int, _P]),
     "qlora_paged_prefetch": (ctypes.c_int, [_P, ctypes.c_size_t, ctypes.c_int32, _P]),

@@ -399,6 +399,41 @@ QLORA_API qlora_status qlora_dropout_add_layernorm_bwd(const void* dY, const voi
 QLORA_API size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols);
 
 /*
+ * The linear layer on an 8-bit integer weight (a frozen or merged weight, for
+ * serving): a scale per token and per output channel, sums in whole numbers.
+ *   quantize   scale[i] = fp32(max_j |X[i,j]| / 127)
+ *              codes[i,j] = the whole number nearest to the real quotient
+ *              X[i,j] / scale[i], ties to even, within -127..127; 0 when the
+ *              scale is 0.  A row that holds an infinity or a NaN gets that as
+ *              its scale and zero codes, so its products are NaN.
+ *   product    Y[m,n] = fp32(sum_k Xq[m,k] Wq[n,k]) x_scale[m] w_scale[n],
+ *              two float32 products and one rounding to dtype
+ * The same call quantizes a weight [N x K] by its rows.  Rows of codes are
+ * `ld` bytes apart: a multiple of 16 that holds a row (QLORA_ERR_INVALID_ARG);
+ * quantization fills a row up to the next multiple of 16 columns with zeros,
+ * and the product does not read past K.  codes are 16-byte aligned, X and Y as
+ * their elements.
+ * qlora_linear_int8_fwd quantizes X into the workspace and multiplies.
+ * M, K, N >= 1, K <= 133144 (sums stay exact in 32 bits), M, N < 2^31 - 512;
+ * otherwise QLORA_ERR_UNSUPPORTED.  Results do not depend on the order of
+ * work.  workspace: at least qlora_int8_workspace_bytes bytes, the first 1024
+ * filled with zeros once before its first use (status word and counters, which
+ * every call leaves at zero); one workspace may serve calls of several sizes in
+ * turn.  After qlora_check_status reports QLORA_ERR_TIMEOUT fill those with
+ * zeros again.  Calls that may overlap need one each.
+ */
+QLORA_API qlora_status qlora_quantize_int8(const void* X, int64_t rows, int64_t cols, int32_t dtype, int8_t* codes,
+                                           int64_t ld, float* scale, void* stream);
+QLORA_API qlora_status qlora_matmul_int8(const int8_t* Xq, int64_t ldx, const float* x_scale, int64_t M, int64_t K,
+                                         int64_t N, const int8_t* Wq, int64_t ldw, const float* w_scale, void* Y,
+                                         int32_t dtype, void* workspace, size_t ws_bytes, void* stream);
+QLORA_API qlora_status qlora_linear_int8_fwd(const void* X, int64_t M, int64_t K, int64_t N, int32_t dtype,
+                                             const int8_t* Wq, int64_t ldw, const float* w_scale, void* Y,
+                                             void* workspace, size_t ws_bytes, void* stream);
+/* Workspace bytes of the two products (0 for an unsupported size). */
+QLORA_API size_t qlora_int8_workspace_bytes(int64_t M, int64_t K, int64_t N);
+
+/*
  * Paged optimizer for the LoRA parameters.  "3. Paged Optimizers" and "AI
  * Glossary: QLoRA", second paragraph: only the LoRA matrices are trained,
  * and their optimizer states live in NVIDIA unified memory so that they can

@@ -33,6 +33,8 @@ Parity status per function (see each module's header):
                             constant gradient, torch.optim.AdamW in float64).
   * dropout / layernorm     pinned (the generator's published known-answer
                             vectors, torch float64 autograd, differences).
+  * quantize_int8 / matmul  pinned (nearest codes in exact rational arithmetic,
+                            sums in Python integers).
 """
 
 from .nf4_ref import (  # noqa: F401
@@ -58,3 +60,4 @@ from .rows_ref import (  # noqa: F401
     layernorm,
     layernorm_grads,
 )
+from .int8_ref import quantize_int8, matmul_int8  # noqa: F401

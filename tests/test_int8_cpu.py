@@ -1,0 +1,110 @@
+"""Host-side refusals of the 8-bit integer linear, and the run arithmetic of
+its few-token kernel (fake pointers are never read)."""
+
+import pytest
+import torch
+
+import bit_quantized_lora_quantize_b200 as q
+from bit_quantized_lora_quantize_b200 import build as qbuild
+
+FAKE = 1 << 20
+BF16, FP32 = 0, 2
+
+
+@pytest.fixture(scope="module")
+def L():
+    qbuild.build()
+    return q.lib()
+
+
+def test_quantize_validation(L):
+    def call(x=FAKE, rows=4, cols=30, dt=BF16, codes=FAKE, ld=32, scale=FAKE):
+        return L.qlora_quantize_int8(x, rows, cols, dt, codes, ld, scale, None)
+    assert call(x=None) == 1 and call(codes=None) == 1 and call(scale=None) == 1
+    assert call(rows=0) == 1 and call(cols=0) == 1 and call(dt=7) == 1
+    assert call(ld=16) == 1 and call(ld=40) == 1  # too short, not a multiple of 16
+    assert call(x=FAKE + 1) == 2 and call(codes=FAKE + 8) == 2 and call(scale=FAKE + 2) == 2
+    assert call(rows=1 << 31) == 3
+
+
+def test_product_validation(L):
+    need = L.qlora_int8_workspace_bytes(4, 30, 8)
+    assert need > 1024
+
+    def mm(x=FAKE, ldx=32, M=4, K=30, N=8, w=FAKE, ldw=32, y=FAKE, dt=BF16, ws=FAKE, nb=need):
+        return L.qlora_matmul_int8(x, ldx, FAKE, M, K, N, w, ldw, FAKE, y, dt, ws, nb, None)
+    assert mm(x=None) == 1 and mm(w=None) == 1 and mm(y=None) == 1 and mm(dt=3) == 1
+    assert mm(M=0) == 1 and mm(K=-1) == 1 and mm(N=0) == 1
+    assert mm(ldx=24) == 1 and mm(ldw=16) == 1
+    assert mm(K=133145, ldx=133152, ldw=133152) == 3 and mm(M=1 << 31) == 3 and mm(N=(1 << 31) - 1) == 3
+    assert mm(x=FAKE + 4) == 2 and mm(y=FAKE + 1) == 2 and mm(dt=FP32, y=FAKE + 2) == 2 and mm(ws=FAKE + 8) == 2
+    assert mm(ws=None) == 4 and mm(nb=need - 1) == 4
+
+    def lin(x=FAKE, M=4, K=30, N=8, dt=BF16, ldw=32, y=FAKE, ws=FAKE, nb=need):
+        return L.qlora_linear_int8_fwd(x, M, K, N, dt, FAKE, ldw, FAKE, y, ws, nb, None)
+    assert lin(x=None) == 1 and lin(y=None) == 1 and lin(M=0) == 1 and lin(dt=-1) == 1 and lin(ldw=31) == 1
+    assert lin(x=FAKE + 1) == 2 and lin(K=1 << 20, ldw=1 << 20) == 3 and lin(ws=None) == 4 and lin(nb=0) == 4
+
+
+def test_workspace_bytes(L):
+    assert L.qlora_int8_workspace_bytes(0, 8, 8) == 0 and L.qlora_int8_workspace_bytes(1, 133145, 8) == 0
+    with pytest.raises(q.QloraError):
+        q.new_int8_workspace(1, 0, 8, "cpu")
+
+
+def run_start(units, block, blocks):
+    return units * block // blocks
+
+
+@pytest.mark.parametrize("tiles,nkb", [(1, 1), (1, 64), (2, 3), (64, 64), (65, 32), (172, 64), (300, 1), (7, 1041)])
+def test_runs_cover_every_unit_once(tiles, nkb):
+    """The schedule of the few-token kernel: equal contiguous runs of (tile,
+    block of depth) units; every split tile is summed from one partial tile
+    per block that holds some of it, in that block's slot 0 (the run begins
+    inside the tile) or 1, and its counter is the block it begins in."""
+    units = tiles * nkb
+    blocks = min(148, -(-units // 4))
+    seen, slots, counters = set(), {}, {}
+    for b in range(blocks):
+        u, end = run_start(units, b, blocks), run_start(units, b + 1, blocks)
+        assert u < end
+        while u < end:
+            tile = u // nkb
+            t0, t1 = tile * nkb, (tile + 1) * nkb
+            stop = min(end, t1)
+            seen.update(range(u, stop))
+            if not (u == t0 and stop == t1):
+                slot = (b, int(u == t0))
+                assert slot not in slots
+                slots[slot] = tile
+                b0 = t0 * blocks // units
+                while b0 + 1 < blocks and run_start(units, b0 + 1, blocks) <= t0:
+                    b0 += 1
+                while b0 > 0 and run_start(units, b0, blocks) > t0:
+                    b0 -= 1
+                counters.setdefault(b0, tile)
+                assert counters[b0] == tile
+                # the summing block's list of partial tiles
+                parts = []
+                for c in range(b0, blocks):
+                    s = run_start(units, c, blocks)
+                    if s >= t1:
+                        break
+                    parts.append((c, int(s <= t0)))
+                assert slot in parts
+            u = stop
+    assert seen == set(range(units))
+    for tile in set(slots.values()):
+        t0, t1 = tile * nkb, (tile + 1) * nkb
+        holders = [(c, int(run_start(units, c, blocks) <= t0)) for c in range(blocks)
+                   if run_start(units, c, blocks) < t1 and run_start(units, c + 1, blocks) > t0]
+        assert all(slots.get(h) == tile for h in holders)
+
+
+def test_binding_refuses_cpu_tensors():
+    x = torch.zeros(2, 16)
+    w = q.PackedInt8(torch.zeros(4, 16, dtype=torch.int8), torch.ones(4), (4, 16))
+    for call in (lambda: q.qlora_quantize_int8(x), lambda: q.qlora_linear_int8_fwd(x, w),
+                 lambda: q.qlora_matmul_int8(w, w)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
