@@ -9,16 +9,14 @@
 //
 // Three kernels:
 // - quantization: one pass, rows in registers, HBM-bound;
-// - up to 128 tokens, bound by reading the weight once: `stream_kernel` takes
-//   128 weight rows as the M side of tcgen05.mma (kind::i8) and the tokens,
-//   padded to 16, 32, 64 or 128, as its N side.  The (row tile, 128-deep
-//   block) units are dealt to one block per SM in equal contiguous runs, so
-//   every SM streams the same number of bytes whatever the shape; a tile whose
-//   units lie in several blocks is summed by the block that finishes last,
-//   from int32 partial tiles in the workspace;
-// - more tokens: `pair_kernel`, persistent CTA pairs (cta_group::2), a 256 x
-//   256 or 256 x 128 tile per pair, TMA ring, two accumulators in TMEM so that
-//   a tile's epilogue runs under the next tile's products.
+// - up to 16 tokens, bound by reading the weight: `token_kernel` streams it
+//   straight into the register fragments of mma.sync;
+// - more tokens: `pair_kernel`, CTA pairs (cta_group::2) with 256 x 256 tiles
+//   fed by a TMA ring; persistent, with two accumulators in TMEM so that a
+//   tile's epilogue runs under the next tile's products, or, where there are
+//   too few tiles for the SMs, two or four pairs of a cluster on each tile.
+//   (A narrower tile does not help: a tcgen05.mma over 128 rows per SM costs
+//   about the same for 16 columns as for 256.)
 #include <algorithm>
 #include <cstdint>
 #include <cuda.h>
@@ -49,29 +47,51 @@ struct QuantArgs {
   int wpr;
 };
 
-// Largest magnitude as bits: NaN orders above infinity, so both survive.
+// Largest magnitude of a lane's eight values, as the bits of the float32:
+// NaN orders above infinity, so both survive.  16-bit types compare in pairs.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 template <typename T>
-__device__ __forceinline__ uint32_t abs_bits(const Raw8<T>& x, int e) {
-  return __float_as_uint(raw_f32(x, e)) & 0x7FFFFFFFu;
+__device__ __forceinline__ uint32_t abs_max(const Raw8<T>& x) {
+  uint32_t m = 0;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, x.w[e] & 0x7FFFFFFFu);
+    return m;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = max_u16x2(m, x.w[e] & 0x7FFF7FFFu);
+    m = max(m & 0xFFFFu, m >> 16);
+    Raw8<T> top;
+    top.w[0] = m;
+    return __float_as_uint(raw_f32(top, 0));
+  }
 }
 
+// Codes of a row with this largest magnitude.  x times the reciprocal of the
+// scale is off by far less than a half; adding 1.5 * 2^23 rounds it to a whole
+// number q, ties to even, whose low byte is the code.  The remainder x - q s is
+// exact in float32 (a multiple of the smaller of the two last places, no
+// larger than s / 2 but for the error of q), so one comparison with s / 2 tells
+// the few codes that may need mending.
 struct RowScale {
   float scale, up, s, inv, half;
+  bool plain;  // neither zero, tiny nor non-finite
   __device__ explicit RowScale(uint32_t bits) {
     scale = __fdiv_rn(__uint_as_float(bits), 127.0f);
+    plain = bits < 0x7F800000u && scale >= 0x1p-100f;
     // A tiny scale is lifted by an exact power of two, so that its
     // reciprocal stays finite.
-    up = scale < 0x1p-100f ? 0x1p64f : 1.0f;
+    up = plain ? 1.0f : 0x1p64f;
     s = scale * up;
     inv = __fdiv_rn(1.0f, s);
     half = 0.5f * s;
-    if (!(bits < 0x7F800000u) || scale == 0.0f) up = s = inv = half = 0.0f;  // all codes 0
+    if (!(bits < 0x7F800000u) || scale == 0.0f) s = 0.0f;  // all codes 0
   }
-  // Nearest whole number to x / scale, ties to even.  The product with the
-  // reciprocal is off by far less than a half, and the remainder x - q s is
-  // exact in float32 (a multiple of the smaller of the two last places, no
-  // larger than s / 2 but for the error of q), so one comparison settles it.
-  __device__ __forceinline__ int code(float x) const {
+  __device__ __noinline__ uint32_t exact_code(float x) const {
     if (s == 0.0f) return 0;
     x *= up;
     float q = rintf(x * inv);
@@ -79,7 +99,29 @@ struct RowScale {
     const bool odd = static_cast<int>(q) & 1;
     if (r > half || (r == half && odd)) q += 1.0f;
     else if (r < -half || (r == -half && odd)) q -= 1.0f;
-    return static_cast<int>(fminf(fmaxf(q, -127.0f), 127.0f));
+    return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(q, -127.0f), 127.0f))) & 0xFFu;
+  }
+  // The codes of eight values, in the low bytes of `c`.  Near ties are not
+  // rare: 127 x / max|x| of two short mantissas often is a half.
+  template <typename T>
+  __device__ __forceinline__ void codes(const Raw8<T>& x, uint32_t (&c)[8]) const {
+    if (!plain) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = exact_code(raw_f32(x, e));
+      return;
+    }
+    float r[8], worst = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = raw_f32(x, e), b = fmaf(v, inv, 12582912.0f);
+      c[e] = __float_as_uint(b);
+      r[e] = fmaf(12582912.0f - b, s, v);
+      worst = fmaxf(worst, fabsf(r[e]));
+    }
+    if (worst < half) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (fabsf(r[e]) > half || (fabsf(r[e]) == half && (c[e] & 1u))) c[e] += r[e] > 0.0f ? 1u : ~0u;
   }
 };
 
@@ -88,18 +130,19 @@ __device__ __forceinline__ void store_codes(const QuantArgs& a, int64_t row, int
                                             const Raw8<T>& x) {
   const int64_t padded = (a.cols + 15) / 16 * 16;  // columns past the end hold 0
   int8_t* out = a.codes + row * a.ld;
+  uint32_t k[8];
+  rs.codes(x, k);
   if constexpr (VEC) {
     const int64_t c = c0 + lane * 8;
-    if (c >= padded) return;
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e >> 2] |= (static_cast<uint32_t>(rs.code(raw_f32(x, e))) & 0xFFu) << (8 * (e & 3));
-    *reinterpret_cast<uint2*>(out + c) = make_uint2(w[0], w[1]);
+    if (c < padded)
+      *reinterpret_cast<uint2*>(out + c) =
+          make_uint2(prmt(prmt(k[0], k[1], 0x0040), prmt(k[2], k[3], 0x0040), 0x5410),
+                     prmt(prmt(k[4], k[5], 0x0040), prmt(k[6], k[7], 0x0040), 0x5410));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int64_t c = c0 + lane + 32 * e;
-      if (c < padded) out[c] = static_cast<int8_t>(rs.code(raw_f32(x, e)));
+      if (c < padded) out[c] = static_cast<int8_t>(k[e]);
     }
   }
 }
@@ -133,10 +176,7 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const QuantArgs a) 
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
-    if (valid && c0 < a.cols) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[g], e));
-    }
+    if (valid && c0 < a.cols) m = max(m, abs_max(x[g]));
   }
   m = row_max(m, red, warp, first, a.wpr);
   if (!valid) return;
@@ -158,11 +198,8 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const QuantArg
   const int64_t row = blockIdx.x;
   const T* xr = static_cast<const T*>(a.x) + row * a.cols;
   uint32_t m = 0;
-  for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256) {
-    const Raw8<T> x = load_cols<false>(xr, c0, a.cols, lane);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x, e));
-  }
+  for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256)
+    m = max(m, abs_max(load_cols<false>(xr, c0, a.cols, lane)));
   const RowScale rs(row_max(m, red, warp, 0, 32));
   if (threadIdx.x == 0) a.scale[row] = rs.scale;
   for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256)
@@ -198,270 +235,155 @@ cudaError_t launch_quantize_int8(int32_t dtype, const QuantArgs& a, cudaStream_t
   return launch_quantize_rows<float>(a, stream);
 }
 
-// ================================================================ few tokens
-constexpr int kStreamMax = 128;   // tokens
-constexpr int kStreamRows = 128;  // weight rows of a tile
-constexpr int kMaxStreamBlocks = 160;
-constexpr int kMinRun = 4;        // units a block takes at least
+// ================================================================ up to 16 tokens
+// Register-fragment products (mma.sync m16n8k32): tokens on the M side, eight
+// weight rows on the N side, the weight straight from global memory into the
+// fragments.  A lane holds 16 consecutive codes of its row for two products;
+// both operands take the same order along the depth, so the sums are the same.
+// The 16 warps of a block share the depth and walk over the block's groups of
+// eight rows together; each group's partial sums meet in shared memory.
+constexpr int kTokenMax = 16;
+constexpr int kTokenWarps = 16;
+constexpr int kTokenBatch = 8;   // 64-deep steps in flight per warp, twice
+constexpr int kTokenSlots = 4;   // row groups between two exchanges
 
-struct StreamArgs {
-  int M, N, nkb, tiles;
-  int64_t units;
+struct TokenArgs {
+  const int8_t* x;
+  const int8_t* w;
   const float* sx;
   const float* sw;
   void* y;
-  int32_t* part;  // [blocks][2][NT][128] partial tiles
-  int* ctr;       // [blocks] units done of the split tile that begins in a block; left at zero
-  int* status;
-  uint64_t wait_ns;
-  int chained;    // the previous kernel quantizes the tokens: the weight may be loaded before it ends
+  int64_t ldx, ldw;
+  int M, K, N, groups;
+  int chained;
 };
 
-template <int NT>
-struct StreamSmem {
-  static constexpr int kW = kStreamRows * kDepth;
-  static constexpr int kX = NT * kDepth;
-  static constexpr int kStage = kW + kX;
-  static constexpr int kStages = std::min(10, 200 * 1024 / kStage);
-  static constexpr int offBar = kStages * kStage;
-  static constexpr int kNumBars = 2 * kStages + 5;  // full, empty; acc full/empty x 2; drain
-  static constexpr int offSlot = offBar + kNumBars * 8;
-  static constexpr int kTotal = offSlot + 16;  // tmem address, abort flag, last flag
-  static constexpr int kDynamic = kTotal + 1024;
-};
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-__device__ __forceinline__ int64_t run_start(int64_t units, int block, int blocks) { return units * block / blocks; }
+// 16 codes from position k of a row; where the row ends inside them, nothing
+// past it is read.
+__device__ __noinline__ uint4 load_tail(const int8_t* row, int k, int K) {
+  uint32_t w[4] = {0, 0, 0, 0};
+  for (int i = 0; i < 16 && k + i < K; ++i)
+    w[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + i])) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 load_stream(const int8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
 template <typename T>
 __device__ __forceinline__ T scaled(int v, float sx, float sw) {
   return from_f32<T>(__fmul_rn(__fmul_rn(static_cast<float>(v), sx), sw));
 }
 
-template <typename T, int NT>
-__global__ void __launch_bounds__(256, 1)
-    stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                  const StreamArgs a) {
-  using L = StreamSmem<NT>;
-  constexpr int kStages = L::kStages;
-  constexpr uint32_t kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::offBar);
-  uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offSlot);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
+// TWO: tokens 8 .. 15 exist.
+template <typename T, bool TWO>
+__global__ void __launch_bounds__(kTokenWarps * 32, 1) token_kernel(const TokenArgs a) {
+  constexpr int kTokens = TWO ? 16 : 8;
+  __shared__ int sums[kTokenSlots][kTokenWarps][kTokens * 8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int g0 = static_cast<int>(static_cast<int64_t>(a.groups) * blockIdx.x / gridDim.x);
+  const int g1 = static_cast<int>(static_cast<int64_t>(a.groups) * (blockIdx.x + 1) / gridDim.x);
+  // Whole 64-deep steps, dealt to the warps; the last warp also takes what is
+  // left of the depth.
+  const int steps = a.K / 64;
+  const int s0 = static_cast<int>(static_cast<int64_t>(steps) * warp / kTokenWarps);
+  const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (warp + 1) / kTokenWarps);
+  const int batches = (s1 - s0 + kTokenBatch - 1) / kTokenBatch;
+  const bool tail = a.K % 64 != 0 && warp == kTokenWarps - 1;
+  // Lanes past the last row or token repeat it; their sums are not stored.
+  const auto row_of = [&](int group) { return a.w + static_cast<int64_t>(min(group * 8 + g, a.N - 1)) * a.ldw; };
+  const int8_t* x0 = a.x + static_cast<int64_t>(min(g, a.M - 1)) * a.ldx;
+  const int8_t* x1 = a.x + static_cast<int64_t>(min(g + 8, a.M - 1)) * a.ldx;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4);
-    }
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    fence_mbarrier_init();
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmX);
-  }
-  if (warp == 2) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int64_t u0 = run_start(a.units, blockIdx.x, gridDim.x), u1 = run_start(a.units, blockIdx.x + 1, gridDim.x);
-  const int n = static_cast<int>(u1 - u0);
+  uint4 next[kTokenBatch];
+  const auto fetch = [&](int group, int batch) {
+    const int s = s0 + batch * kTokenBatch;
+    const int8_t* p = row_of(group) + s * 64 + q * 16;
+#pragma unroll
+    for (int i = 0; i < kTokenBatch; ++i)
+      if (s + i < s1) next[i] = load_stream(p + i * 64);
+  };
+  // The weight is ready before the kernel that quantizes the tokens started.
+  if (!a.chained) griddep_wait();
+  if (g0 < g1) fetch(g0, 0);
+  if (a.chained) griddep_wait();
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const WaitCtx ctx{abort_flag, a.status, 51, a.wait_ns};
-      const auto load_w = [&](int i) {
-        const int64_t u = u0 + i;
-        const int tile = static_cast<int>(u / a.nkb), kb = static_cast<int>(u - static_cast<int64_t>(tile) * a.nkb);
-        mbar_arrive_expect_tx(&full[i % kStages], L::kStage);
-        tma_load_2d(&tmW, &full[i % kStages], smem + (i % kStages) * L::kStage, kb * kDepth, tile * kStreamRows);
-      };
-      const auto load_x = [&](int i) {
-        const int kb = static_cast<int>((u0 + i) % a.nkb);
-        tma_load_2d(&tmX, &full[i % kStages], smem + (i % kStages) * L::kStage + L::kW, kb * kDepth, 0);
-      };
-      // The weight is ready before the kernel that quantizes the tokens
-      // started; the codes only once it has ended.
-      const int ahead = min(n, kStages);
-      if (!a.chained) griddep_wait();
-      for (int i = 0; i < ahead; ++i) load_w(i);
-      if (a.chained) griddep_wait();
-      for (int i = 0; i < ahead; ++i) load_x(i);
-      int issued = ahead;
-      for (int i = ahead; i < n; ++i) {
-        if (!mbar_wait(&empty[i % kStages], ((i / kStages) & 1) ^ 1, ctx)) break;
-        load_w(i);
-        load_x(i);
-        ++issued;
-      }
-      if (*abort_flag)
-        for (int i = max(0, issued - kStages); i < issued; ++i) mbar_drain(&full[i % kStages], (i / kStages) & 1);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      const WaitCtx ctx{abort_flag, a.status, 52, a.wait_ns};
-      constexpr uint32_t idesc = idesc_s8_s32(kStreamRows, NT);
-      bool ok = true;
-      int seg = -1, prev = -1;
-      for (int i = 0; i < n && ok; ++i) {
-        const int tile = static_cast<int>((u0 + i) / a.nkb);
-        const bool first = tile != prev;
-        if (first) {
-          prev = tile;
-          ++seg;
-          if (!(ok = mbar_wait(&acc_empty[seg & 1], ((seg >> 1) & 1) ^ 1, ctx))) break;
-        }
-        if (!(ok = mbar_wait(&full[i % kStages], (i / kStages) & 1, ctx))) break;
-        tc_fence_after();
-        const uint32_t w = smem_u32(smem + (i % kStages) * L::kStage), x = w + L::kW;
+  int c[4] = {0, 0, 0, 0};
+  for (int from = g0; from < g1; from += kTokenSlots) {
+    const int to = min(g1, from + kTokenSlots);
+    for (int group = from; group < to; ++group) {
+      for (int batch = 0; batch < batches; ++batch) {
+        uint4 w[kTokenBatch];
 #pragma unroll
-        for (int k = 0; k < kDepth / 32; ++k)
-          umma_s8(tmem + (seg & 1) * NT, smem_desc_sw128(w + k * 32, 16, 1024), smem_desc_sw128(x + k * 32, 16, 1024),
-                  idesc, !first || k > 0);
-        umma_commit(&empty[i % kStages]);
-        if (i + 1 == n || static_cast<int>((u0 + i + 1) / a.nkb) != tile) umma_commit(&acc_full[seg & 1]);
-      }
-      if (!ok) {  // the products already issued must end before the block leaves
-        umma_commit(drain);
-        mbar_drain(drain, 0);
-      }
-    }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ epilogue
-    const WaitCtx ctx{abort_flag, a.status, 53, a.wait_ns};
-    const int q = warp & 3, t = q * 32 + lane;  // weight row of the tile
-    griddep_wait();                             // sx, the partial tiles and Y
-    int seg = 0;
-    bool ok = true;  // after a wait that gave up the warp only keeps the barriers below
-    for (int64_t u = u0; u < u1; ++seg) {
-      const int tile = static_cast<int>(u / a.nkb);
-      const int64_t t0 = static_cast<int64_t>(tile) * a.nkb, t1 = t0 + a.nkb;
-      const int64_t end = min(u1, t1);
-      ok = __all_sync(kAll, ok && mbar_wait(&acc_full[seg & 1], (seg >> 1) & 1, ctx));
-      tc_fence_after();
-      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + (seg & 1) * NT;
-      const int row = tile * kStreamRows + t;
-      const float sw = row < a.N ? __ldg(a.sw + row) : 0.0f;
-      T* y = static_cast<T*>(a.y) + row;
-      const bool whole = u == t0 && end == t1;
-      int32_t* mine = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (u == t0)) * NT * kStreamRows + t;
+        for (int i = 0; i < kTokenBatch; ++i) w[i] = next[i];
+        if (batch + 1 < batches) fetch(group, batch + 1);
+        else if (group + 1 < g1) fetch(group + 1, 0);
+        const int s = s0 + batch * kTokenBatch, at = s * 64 + q * 16;
 #pragma unroll
-      for (int c = 0; c < NT / 16; ++c) {
-        if (!ok || c * 16 >= a.M) break;
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(acc + c * 16, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int m = c * 16 + e;
-          if (m >= a.M) break;
-          if (!whole) mine[m * kStreamRows] = static_cast<int32_t>(v[e]);
-          else if (row < a.N) y[static_cast<int64_t>(m) * a.N] = scaled<T>(static_cast<int>(v[e]), __ldg(a.sx + m), sw);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[seg & 1]);
-      if (!whole) {
-        // The block whose units complete the tile adds up all partial tiles.
-        __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        // The block this tile begins in: the last whose run starts at or
-        // before t0.  It begins no other tile that it does not finish, so the
-        // tile's counter is that block's.
-        int b0 = static_cast<int>(t0 * gridDim.x / a.units);
-        while (b0 + 1 < static_cast<int>(gridDim.x) && run_start(a.units, b0 + 1, gridDim.x) <= t0) ++b0;
-        while (b0 > 0 && run_start(a.units, b0, gridDim.x) > t0) --b0;
-        if (t == 0) {
-          const int add = static_cast<int>(end - u);
-          const bool last = ok && atomicAdd(a.ctr + b0, add) + add == a.nkb;
-          *last_flag = last;
-          if (last) a.ctr[b0] = 0;  // nobody else adds to this tile
-          __threadfence();
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (*last_flag) {
-          for (int m0 = 0; m0 < a.M; m0 += 8) {
-            int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int b = b0; b < static_cast<int>(gridDim.x); ++b) {
-              const int64_t s = run_start(a.units, b, gridDim.x);
-              if (s >= t1) break;
-              const int32_t* p = a.part + (static_cast<int64_t>(b) * 2 + (s <= t0)) * NT * kStreamRows + t;
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (m0 + e < a.M) sum[e] += __ldcg(p + (m0 + e) * kStreamRows);
-            }
-            if (row < a.N) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (m0 + e < a.M) y[static_cast<int64_t>(m0 + e) * a.N] = scaled<T>(sum[e], __ldg(a.sx + m0 + e), sw);
-            }
+        for (int i = 0; i < kTokenBatch; ++i) {
+          if (s + i < s1) {
+            const uint4 x = *reinterpret_cast<const uint4*>(x0 + at + i * 64);
+            const uint4 z = TWO ? *reinterpret_cast<const uint4*>(x1 + at + i * 64) : make_uint4(0, 0, 0, 0);
+            mma_s8(c, x.x, z.x, x.y, z.y, w[i].x, w[i].y);
+            mma_s8(c, x.z, z.z, x.w, z.w, w[i].z, w[i].w);
           }
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // last_flag is free again
       }
-      u = end;
+      if (tail) {
+        const int at = steps * 64 + q * 16;
+        const uint4 w = load_tail(row_of(group), at, a.K), x = load_tail(x0, at, a.K);
+        const uint4 z = TWO ? load_tail(x1, at, a.K) : make_uint4(0, 0, 0, 0);
+        mma_s8(c, x.x, z.x, x.y, z.y, w.x, w.y);
+        mma_s8(c, x.z, z.z, x.w, z.w, w.z, w.w);
+      }
+      // c[0], c[1]: token g, rows 2 q and 2 q + 1 of the group; c[2], c[3]: token g + 8
+      int* out = sums[group - from][warp];
+      *reinterpret_cast<int2*>(out + g * 8 + 2 * q) = make_int2(c[0], c[1]);
+      if (TWO) *reinterpret_cast<int2*>(out + (g + 8) * 8 + 2 * q) = make_int2(c[2], c[3]);
+      c[0] = c[1] = c[2] = c[3] = 0;
     }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 2) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    __syncthreads();
+    for (int i = threadIdx.x; i < (to - from) * 8 * a.M; i += kTokenWarps * 32) {
+      const int rows = (to - from) * 8, m = i / rows, r = i - m * rows, row = from * 8 + r;
+      int sum = 0;
+#pragma unroll
+      for (int v = 0; v < kTokenWarps; ++v) sum += sums[r >> 3][v][m * 8 + (r & 7)];
+      if (row < a.N)
+        static_cast<T*>(a.y)[static_cast<int64_t>(m) * a.N + row] = scaled<T>(sum, __ldg(a.sx + m), __ldg(a.sw + row));
+    }
+    if (to < g1) __syncthreads();
   }
 }
 
-int stream_width(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
-
-template <typename T, int NT>
-cudaError_t launch_stream_width(const CUtensorMap& w, const CUtensorMap& x, const StreamArgs& a, int grid,
-                                cudaStream_t stream) {
-  using L = StreamSmem<NT>;
-  static_assert(L::kDynamic <= 232448, "shared memory budget");
-  auto kern = stream_kernel<T, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynamic);
-  if (e != cudaSuccess) return e;
+template <typename T>
+cudaError_t launch_token(const TokenArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.dynamicSmemBytes = L::kDynamic;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(a.groups, device_sm_count())), 1, 1);
+  cfg.blockDim = dim3(kTokenWarps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr = pdl_attribute();
   cfg.attrs = &attr;
   cfg.numAttrs = a.chained ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, w, x, a);
+  return a.M > 8 ? cudaLaunchKernelEx(&cfg, token_kernel<T, true>, a)
+                 : cudaLaunchKernelEx(&cfg, token_kernel<T, false>, a);
 }
 
-template <typename T>
-cudaError_t launch_stream(const CUtensorMap& w, const CUtensorMap& x, const StreamArgs& a, int grid, int width,
-                          cudaStream_t stream) {
-  switch (width) {
-    case 16: return launch_stream_width<T, 16>(w, x, a, grid, stream);
-    case 32: return launch_stream_width<T, 32>(w, x, a, grid, stream);
-    case 64: return launch_stream_width<T, 64>(w, x, a, grid, stream);
-    default: return launch_stream_width<T, 128>(w, x, a, grid, stream);
-  }
-}
-
-// ================================================================ many tokens
+// ================================================================ more tokens
 constexpr int kPairTokens = 256;  // rows of a pair's tile (tokens), 128 per CTA
+constexpr int kPairCols = 256;    // its columns (weight rows), 128 per CTA
+constexpr int kMaxPairs = 80;     // of a launch that splits its tiles
 
 struct PairGemmArgs {
   int M, N, nkb, tiles_m, tiles_n, tiles, group_rows;
@@ -469,20 +391,23 @@ struct PairGemmArgs {
   const float* sw;
   void* y;
   int vec;        // rows of Y are whole 16-byte vectors
+  int split;      // pairs that share a tile
+  int* ctr;       // [tiles][2] parts of a split tile that are done; left at zero
+  int32_t* part;  // [tiles][split][2] partial sums of 128 rows, [column][row]
   int* status;
   uint64_t wait_ns;
 };
 
-template <int BN>
 struct PairGemmSmem {
-  static constexpr int kX = 128 * kDepth;       // this CTA's tokens
-  static constexpr int kW = BN / 2 * kDepth;    // this CTA's half of the weight rows
-  static constexpr int kStage = kX + kW;
-  static constexpr int kStages = std::min(8, 200 * 1024 / kStage);
+  static constexpr int kHalf = 128 * kDepth;  // this CTA's tokens; as many bytes of its weight rows follow
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = 6;
   static constexpr int offBar = kStages * kStage;
   static constexpr int kNumBars = 2 * kStages + 5;
   static constexpr int offSlot = offBar + kNumBars * 8;
-  static constexpr int kTotal = offSlot + 16;
+  static constexpr int offTurn = (offSlot + 16 + 15) / 16 * 16;  // per epilogue warp 32 x 33 floats
+  static constexpr int offScale = offTurn + 4 * 32 * 33 * 4;  // per epilogue warp the tile's column scales
+  static constexpr int kTotal = offScale + 4 * kPairCols * 4;
   static constexpr int kDynamic = kTotal + 1024;
 };
 
@@ -495,13 +420,65 @@ __device__ __forceinline__ void pair_tile(const PairGemmArgs& a, int tile, int& 
   tm = g * a.group_rows + at - tn * rows;
 }
 
-template <typename T, int BN>
+// The scales of columns col0 .. col0 + n - 1 into a warp's shared memory.
+__device__ __forceinline__ void load_scales(const PairGemmArgs& a, int col0, int n, float* to) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int c = lane; c < n; c += 32) to[c] = col0 + c < a.N ? __ldg(a.sw + col0 + c) : 0.0f;
+}
+
+// 32 columns of a warp's 32 rows of Y from their whole-number sums; `sw` holds
+// the columns' scales.
+template <typename T>
+__device__ __forceinline__ void store_scaled(const PairGemmArgs& a, int row, int col0, const uint32_t (&v)[32], float sx,
+                                             const float* sw, float* turn) {
+  const int lane = threadIdx.x & 31;
+  float f[32];
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(sw + e);
+    f[e] = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(v[e])), sx), s.x);
+    f[e + 1] = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(v[e + 1])), sx), s.y);
+    f[e + 2] = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(v[e + 2])), sx), s.z);
+    f[e + 3] = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(v[e + 3])), sx), s.w);
+  }
+  if (a.vec) {
+    if (row < a.M) {
+      T* out = static_cast<T*>(a.y) + static_cast<int64_t>(row) * a.N;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (col0 + g * 8 < a.N) {
+          const float w8[8] = {f[g * 8],     f[g * 8 + 1], f[g * 8 + 2], f[g * 8 + 3],
+                               f[g * 8 + 4], f[g * 8 + 5], f[g * 8 + 6], f[g * 8 + 7]};
+          store_group(out + col0 + g * 8, raw_from<T>(w8));
+        }
+      }
+    }
+  } else {
+    // Ragged rows: turn the 32 x 32 block in shared memory, so that a warp
+    // stores 32 neighbours of one row at a time.
+#pragma unroll
+    for (int e = 0; e < 32; ++e) turn[lane * 33 + e] = f[e];
+    __syncwarp();
+    T* to = static_cast<T*>(a.y) + static_cast<int64_t>(row - lane) * a.N + col0 + lane;
+    const int rows = min(32, a.M - (row - lane));
+    if (col0 + lane < a.N)
+      for (int r = 0; r < rows; ++r) to[static_cast<int64_t>(r) * a.N] = from_f32<T>(turn[r * 33 + lane]);
+    __syncwarp();
+  }
+}
+
+// Without SPLIT: persistent pairs, one tile after the other.  With it: `split`
+// pairs on each tile, each a part of the depth; every CTA leaves its partial
+// sums in the workspace and the last of a tile's `split` CTAs of one rank adds
+// them up.  Nobody waits for another pair.
+template <typename T, bool SPLIT>
 __global__ void __launch_bounds__(256, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                 const PairGemmArgs a) {
-  using L = PairGemmSmem<BN>;
+  using L = PairGemmSmem;
   constexpr int kStages = L::kStages;
-  constexpr uint32_t kTmemCols = 2 * BN;
+  constexpr uint32_t kTmemCols = 2 * kPairCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::offBar);  // leader: both CTAs' bytes
@@ -511,6 +488,7 @@ __global__ void __launch_bounds__(256, 1)
   uint64_t* drain = acc_empty + 2;                                 // leader
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();  // 0 = leader
@@ -538,7 +516,10 @@ __global__ void __launch_bounds__(256, 1)
   cluster_sync_all();  // the leader's barriers exist before the peer uses them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int pairs = static_cast<int>(gridDim.x >> 1), first = static_cast<int>(blockIdx.x >> 1);
+  const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+  const int first = SPLIT ? pair / a.split : pair, stride = SPLIT ? a.tiles : pairs;
+  const int share = SPLIT ? pair - first * a.split : 0;
+  const int kb0 = SPLIT ? a.nkb * share / a.split : 0, kb1 = SPLIT ? a.nkb * (share + 1) / a.split : a.nkb;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -546,18 +527,19 @@ __global__ void __launch_bounds__(256, 1)
       const WaitCtx ctx{abort_flag, a.status, 54, a.wait_ns};
       int i = 0;
       bool ok = true;
-      for (int tile = first; tile < a.tiles && ok; tile += pairs) {
+      griddep_wait();
+      for (int tile = first; tile < a.tiles && ok; tile += stride) {
         int tm, tn;
         pair_tile(a, tile, tm, tn);
         const int x_row = tm * kPairTokens + static_cast<int>(rank) * 128;
-        const int w_row = tn * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kb = 0; kb < a.nkb; ++kb, ++i) {
+        const int w_row = tn * kPairCols + static_cast<int>(rank) * 128;
+        for (int kb = kb0; kb < kb1; ++kb, ++i) {
           const int s = i % kStages;
           if (!(ok = mbar_wait(&empty[s], ((i / kStages) & 1) ^ 1, ctx))) break;
           const uint32_t bar = map_rank(&full[s], 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
           tma_load_2d_pair(&tmX, bar, smem + s * L::kStage, kb * kDepth, x_row);
-          tma_load_2d_pair(&tmW, bar, smem + s * L::kStage + L::kX, kb * kDepth, w_row);
+          tma_load_2d_pair(&tmW, bar, smem + s * L::kStage + L::kHalf, kb * kDepth, w_row);
         }
       }
       if (*abort_flag && rank == 0)
@@ -567,21 +549,21 @@ __global__ void __launch_bounds__(256, 1)
     // ------------------------------------------------------------ MMA (leader)
     if (lane == 0 && rank == 0) {
       const WaitCtx ctx{abort_flag, a.status, 55, a.wait_ns};
-      constexpr uint32_t idesc = idesc_s8_s32(kPairTokens, BN);
+      constexpr uint32_t idesc = idesc_s8_s32(kPairTokens, kPairCols);
       int i = 0, seg = 0;
       bool ok = true;
-      for (int tile = first; tile < a.tiles && ok; tile += pairs, ++seg) {
+      for (int tile = first; tile < a.tiles && ok; tile += stride, ++seg) {
         if (!(ok = mbar_wait(&acc_empty[seg & 1], ((seg >> 1) & 1) ^ 1, ctx))) break;
         tc_fence_after();
-        for (int kb = 0; kb < a.nkb; ++kb, ++i) {
+        for (int kb = kb0; kb < kb1; ++kb, ++i) {
           const int s = i % kStages;
           if (!(ok = mbar_wait(&full[s], (i / kStages) & 1, ctx))) break;
           tc_fence_after();
-          const uint32_t x = smem_u32(smem + s * L::kStage), w = x + L::kX;
+          const uint32_t x = smem_u32(smem + s * L::kStage), w = x + L::kHalf;
 #pragma unroll
           for (int k = 0; k < kDepth / 32; ++k)
-            umma_s8_pair(tmem + (seg & 1) * BN, smem_desc_sw128(x + k * 32, 16, 1024),
-                         smem_desc_sw128(w + k * 32, 16, 1024), idesc, kb > 0 || k > 0);
+            umma_s8_pair(tmem + (seg & 1) * kPairCols, smem_desc_sw128(x + k * 32, 16, 1024),
+                         smem_desc_sw128(w + k * 32, 16, 1024), idesc, kb > kb0 || k > 0);
           umma_commit_pair(&empty[s]);
         }
         if (ok) umma_commit_pair(&acc_full[seg & 1]);
@@ -595,49 +577,92 @@ __global__ void __launch_bounds__(256, 1)
     // ------------------------------------------------------------ epilogue
     const WaitCtx ctx{abort_flag, a.status, 56, a.wait_ns};
     const int q = warp & 3;
+    float* turn = reinterpret_cast<float*>(smem + L::offTurn) + q * 32 * 33;
+    float* sw = reinterpret_cast<float*>(smem + L::offScale) + q * kPairCols;
+    griddep_wait();
     int seg = 0;
-    for (int tile = first; tile < a.tiles; tile += pairs, ++seg) {
+    for (int tile = first; tile < a.tiles && !SPLIT; tile += stride, ++seg) {
       int tm, tn;
       pair_tile(a, tile, tm, tn);
       const int row = tm * kPairTokens + static_cast<int>(rank) * 128 + q * 32 + lane;
-      const bool in = row < a.M;
-      const float sx = in ? __ldg(a.sx + row) : 0.0f;
-      T* out = static_cast<T*>(a.y) + static_cast<int64_t>(row) * a.N;
+      const float sx = row < a.M ? __ldg(a.sx + row) : 0.0f;
+      __syncwarp();
+      load_scales(a, tn * kPairCols, kPairCols, sw);
+      __syncwarp();
       if (!__all_sync(kAll, mbar_wait(&acc_full[seg & 1], (seg >> 1) & 1, ctx))) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + (seg & 1) * BN;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + (seg & 1) * kPairCols;
+      // Columns of this tile that exist, for warps with rows that do.
+      const int cols = row - lane < a.M ? min(kPairCols, a.N - tn * kPairCols) : 0;
 #pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
-        const int col0 = tn * BN + c * 32;
-        if (col0 >= a.N) break;
+      for (int c = 0; c < cols; c += 32) {
         uint32_t v[32];
-        tmem_ld_32x32b_x32(acc + c * 32, v);
-        const float my = col0 + lane < a.N ? __ldg(a.sw + col0 + lane) : 0.0f;
+        tmem_ld_32x32b_x32(acc + c, v);
         tmem_wait_ld();
-        float f[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          f[e] = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(v[e])), sx), __shfl_sync(kAll, my, e));
-        if (in) {
-          if (a.vec) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              if (col0 + g * 8 < a.N) {
-                const float w8[8] = {f[g * 8], f[g * 8 + 1], f[g * 8 + 2], f[g * 8 + 3],
-                                     f[g * 8 + 4], f[g * 8 + 5], f[g * 8 + 6], f[g * 8 + 7]};
-                store_group(out + col0 + g * 8, raw_from<T>(w8));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (col0 + e < a.N) out[col0 + e] = from_f32<T>(f[e]);
-          }
-        }
+        store_scaled<T>(a, row, tn * kPairCols + c, v, sx, sw + c, turn);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_rank(&acc_empty[seg & 1], 0));
+    }
+    if (SPLIT) mbar_wait(&acc_full[0], 0, ctx);
+  }
+  if (SPLIT) {
+    // The products are done: all eight warps hand over or add up, each 32 rows
+    // of half of the columns.
+    __syncthreads();
+    tc_fence_after();
+    constexpr int kPart = kPairCols * 128;
+    const bool ok = *abort_flag == 0;
+    const int q = warp & 3;
+    int tm, tn;
+    pair_tile(a, first, tm, tn);
+    const int row = tm * kPairTokens + static_cast<int>(rank) * 128 + q * 32 + lane;
+    const int half = (warp >> 2) * (kPairCols / 2);
+    const int cols = row - lane < a.M ? min(kPairCols / 2, a.N - tn * kPairCols - half) : 0;
+    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + half;
+    int32_t* part = a.part + (static_cast<int64_t>(first) * a.split * 2 + rank) * kPart + half * 128 + q * 32 + lane;
+    const float sx = row < a.M ? __ldg(a.sx + row) : 0.0f;
+    float* sw = reinterpret_cast<float*>(smem + L::offScale) + warp * (kPairCols / 2);
+    load_scales(a, tn * kPairCols + half, kPairCols / 2, sw);
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(acc + c, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) __stcg(part + share * 2 * kPart + (c + e) * 128, static_cast<int32_t>(v[e]));
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const bool last = ok && atomicAdd(a.ctr + first * 2 + rank, 1) + 1 == a.split;
+      if (last) a.ctr[first * 2 + rank] = 0;  // nobody else adds to it
+      *last_flag = last;
+      __threadfence();
+    }
+    __syncthreads();
+    if (*last_flag) {
+      float* turn = reinterpret_cast<float*>(smem) + warp * 32 * 33;  // the ring is free
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 64) {
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(acc + c, v[0]);
+        tmem_ld_32x32b_x32(acc + c + 32, v[1]);
+        tmem_wait_ld();
+#pragma unroll 1
+        for (int d = 1; d < a.split; ++d) {
+          const int p = share + d < a.split ? share + d : share + d - a.split;
+          int32_t o[64];
+#pragma unroll
+          for (int e = 0; e < 64; ++e) o[e] = __ldcg(part + p * 2 * kPart + (c + e) * 128);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) v[e >> 5][e & 31] += static_cast<uint32_t>(o[e]);
+        }
+        store_scaled<T>(a, row, tn * kPairCols + half + c, v[0], sx, sw + c, turn);
+        if (c + 32 < cols)
+          store_scaled<T>(a, row, tn * kPairCols + half + c + 32, v[1], sx, sw + c + 32, turn);
+      }
     }
   }
   tc_fence_before();
@@ -649,12 +674,13 @@ __global__ void __launch_bounds__(256, 1)
   }
 }
 
-template <typename T, int BN>
-cudaError_t launch_pair_gemm(const CUtensorMap& x, const CUtensorMap& w, const PairGemmArgs& a, int pairs,
+template <typename T, bool SPLIT>
+cudaError_t launch_pair_gemm(const CUtensorMap& x, const CUtensorMap& w, const PairGemmArgs& a, int pairs, bool chained,
                              cudaStream_t stream) {
-  using L = PairGemmSmem<BN>;
+  using L = PairGemmSmem;
   static_assert(L::kDynamic <= 232448, "shared memory budget");
-  auto kern = pair_kernel<T, BN>;
+  static_assert(L::offBar % 8 == 0 && L::offScale % 16 == 0, "barriers, and scales read as vectors");
+  auto kern = pair_kernel<T, SPLIT>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kDynamic);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -662,14 +688,32 @@ cudaError_t launch_pair_gemm(const CUtensorMap& x, const CUtensorMap& w, const P
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = L::kDynamic;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1] = pdl_attribute();
+  cfg.attrs = attr;
+  cfg.numAttrs = chained ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, x, w, a);
+}
+
+// Pairs per tile.  A 128-deep block takes a pair about 0.33 us and handing
+// over and adding partial sums about 7 us (200 tokens on 8192 rows: 26.2 us
+// with two pairs at a depth of 8192, 28.3 with one; 15.8 against 11.6 at 2048).
+int pair_split(int64_t tiles, int nkb, int sms) {
+  const int pairs = std::min(std::max(1, sms / 2), kMaxPairs);
+  int best = 1;
+  double best_us = 0.33 * nkb;
+  for (int s = 2; s * tiles <= pairs && s <= nkb; ++s) {
+    const double us = 0.33 * ((nkb + s - 1) / s) + 7.0;
+    if (us < best_us) {
+      best = s;
+      best_us = us;
+    }
+  }
+  return best;
 }
 
 // ================================================================ host
@@ -678,26 +722,28 @@ constexpr size_t kStatusBytes = 256;
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 int64_t padded_depth(int64_t K) { return (K + 15) / 16 * 16; }
 
-// [status][counters of the few-token tiles][codes and scales of X][partial
-// tiles].  Only the first two, of one size for all shapes, need zeros.
+// [status][counters of split tiles][codes and scales of X][partial sums of
+// split tiles].  Only the first two, of one size for all shapes, need zeros.
 struct Int8Layout {
-  size_t ctr, part, codes, scale, total;
+  size_t ctr, codes, scale, part, total;
 };
 
-Int8Layout int8_layout(int64_t M, int64_t K) {
+Int8Layout int8_layout(int64_t M, int64_t K, int64_t N) {
   Int8Layout l{};
   l.ctr = kStatusBytes;
-  l.codes = l.ctr + round256(kMaxStreamBlocks * 4);
+  l.codes = l.ctr + 768;
+  static_assert(kMaxPairs * 2 * 4 <= 768, "a counter per tile and rank");
   l.scale = l.codes + round256(static_cast<size_t>(M) * padded_depth(K));
   l.part = l.scale + round256(static_cast<size_t>(M) * 4);
   l.total = l.part;
-  if (M <= kStreamMax) l.total += static_cast<size_t>(kMaxStreamBlocks) * 2 * stream_width(M) * kStreamRows * 4;
+  const int64_t tiles = ((M + kPairTokens - 1) / kPairTokens) * ((N + kPairCols - 1) / kPairCols);
+  if (M > kTokenMax && 2 * tiles <= kMaxPairs) l.total += static_cast<size_t>(kMaxPairs) * kPairTokens * kPairCols * 4;
   return l;
 }
 
 qlora_status check_int8_shape(int64_t M, int64_t K, int64_t N) {
   if (M <= 0 || K <= 0 || N <= 0) return QLORA_ERR_INVALID_ARG;
-  if (M >= (int64_t(1) << 31) - 512 || N >= (int64_t(1) << 31) - 512 || K > kMaxDepth) return QLORA_ERR_UNSUPPORTED;
+  if (M >= (int64_t(1) << 31) - 32768 || N >= (int64_t(1) << 31) - 32768 || K > kMaxDepth) return QLORA_ERR_UNSUPPORTED;
   // tiles and rows are counted in 32 bits
   if ((M / 128 + 1) * (N / 128 + 1) >= (int64_t(1) << 31)) return QLORA_ERR_UNSUPPORTED;
   return QLORA_OK;
@@ -707,61 +753,37 @@ template <typename T>
 cudaError_t launch_product(const int8_t* xq, int64_t ldx, const float* sx, int64_t M, int64_t K, int64_t N,
                            const int8_t* wq, int64_t ldw, const float* sw, T* y, uint8_t* ws, bool chained,
                            cudaStream_t stream) {
-  const Int8Layout l = int8_layout(M, K);
   const int nkb = static_cast<int>((K + kDepth - 1) / kDepth);
-  CUtensorMap mx, mw;
-  if (M <= kStreamMax) {
-    const int width = stream_width(M);
-    if (!make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, K, N, ldw, kDepth, kStreamRows,
-                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, ldx, kDepth, width, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
-    StreamArgs a{};
-    a.M = static_cast<int>(M);
-    a.N = static_cast<int>(N);
-    a.nkb = nkb;
-    a.tiles = static_cast<int>((N + kStreamRows - 1) / kStreamRows);
-    a.units = static_cast<int64_t>(a.tiles) * nkb;
-    a.sx = sx;
-    a.sw = sw;
-    a.y = y;
-    a.ctr = reinterpret_cast<int*>(ws + l.ctr);
-    a.part = reinterpret_cast<int32_t*>(ws + l.part);
-    a.status = reinterpret_cast<int*>(ws);
-    a.wait_ns = wait_limit_ns();
-    a.chained = chained ? 1 : 0;
-    const int64_t want = (a.units + kMinRun - 1) / kMinRun;
-    const int grid = static_cast<int>(std::min<int64_t>(want, std::min(device_sm_count(), kMaxStreamBlocks)));
-    return launch_stream<T>(mw, mx, a, grid, width, stream);
+  if (M <= kTokenMax) {
+    const TokenArgs a{xq,  wq,  sx, sw, y, ldx, ldw, static_cast<int>(M), static_cast<int>(K), static_cast<int>(N),
+                      static_cast<int>((N + 7) / 8), chained ? 1 : 0};
+    return launch_token<T>(a, stream);
   }
-  PairGemmArgs a{};
-  const int tiles_m = static_cast<int>((M + kPairTokens - 1) / kPairTokens);
-  const int pairs = std::max(1, device_sm_count() / 2);
-  // The narrower tile when it fills the last wave of pairs better.
-  const auto waves = [&](int bn) {
-    const int64_t tiles = static_cast<int64_t>(tiles_m) * ((N + bn - 1) / bn);
-    return (tiles + pairs - 1) / pairs * bn;
-  };
-  const int bn = waves(128) < waves(256) ? 128 : 256;
+  CUtensorMap mx, mw;
   if (!make_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K, M, ldx, kDepth, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, K, N, ldw, kDepth, bn / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+      !make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, K, N, ldw, kDepth, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  const int sms = device_sm_count();
+  PairGemmArgs a{};
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
   a.nkb = nkb;
-  a.tiles_m = tiles_m;
-  a.tiles_n = static_cast<int>((N + bn - 1) / bn);
+  a.tiles_m = static_cast<int>((M + kPairTokens - 1) / kPairTokens);
+  a.tiles_n = static_cast<int>((N + kPairCols - 1) / kPairCols);
   a.tiles = a.tiles_m * a.tiles_n;
-  a.group_rows = std::min(tiles_m, 8);
+  a.group_rows = std::min(a.tiles_m, 8);
   a.sx = sx;
   a.sw = sw;
   a.y = y;
   a.vec = N % 8 == 0 && aligned_to(y, 16);
   a.status = reinterpret_cast<int*>(ws);
   a.wait_ns = wait_limit_ns();
-  const int grid = std::min(a.tiles, pairs);
-  return bn == 128 ? launch_pair_gemm<T, 128>(mx, mw, a, grid, stream)
-                   : launch_pair_gemm<T, 256>(mx, mw, a, grid, stream);
+  const Int8Layout l = int8_layout(M, K, N);
+  a.split = pair_split(a.tiles, nkb, sms);
+  a.ctr = reinterpret_cast<int*>(ws + l.ctr);
+  a.part = reinterpret_cast<int32_t*>(ws + l.part);
+  if (a.split > 1) return launch_pair_gemm<T, true>(mx, mw, a, a.tiles * a.split, chained, stream);
+  return launch_pair_gemm<T, false>(mx, mw, a, std::min(a.tiles, std::max(1, sms / 2)), chained, stream);
 }
 
 cudaError_t launch_matmul_int8(int32_t dtype, const int8_t* xq, int64_t ldx, const float* sx, int64_t M, int64_t K,
@@ -801,7 +823,7 @@ qlora_status qlora_quantize_int8(const void* X, int64_t rows, int64_t cols, int3
 }
 
 size_t qlora_int8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  return check_int8_shape(M, K, N) == QLORA_OK ? int8_layout(M, K).total : 0;
+  return check_int8_shape(M, K, N) == QLORA_OK ? int8_layout(M, K, N).total : 0;
 }
 
 qlora_status qlora_matmul_int8(const int8_t* Xq, int64_t ldx, const float* x_scale, int64_t M, int64_t K, int64_t N,
@@ -814,7 +836,7 @@ qlora_status qlora_matmul_int8(const int8_t* Xq, int64_t ldx, const float* x_sca
   if (!aligned16(Xq) || !aligned16(Wq) || !aligned_to(x_scale, 4) || !aligned_to(w_scale, 4) ||
       !aligned_to(Y, dtype_bytes(dtype)))
     return QLORA_ERR_ALIGNMENT;
-  if (!workspace || ws_bytes < int8_layout(M, K).total) return QLORA_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < int8_layout(M, K, N).total) return QLORA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(st, "matmul_int8", 1);
@@ -834,7 +856,7 @@ qlora_status qlora_linear_int8_fwd(const void* X, int64_t M, int64_t K, int64_t 
   if (bad_stride(ldw, K)) return QLORA_ERR_INVALID_ARG;
   const int es = dtype_bytes(dtype);
   if (!aligned_to(X, es) || !aligned_to(Y, es) || !aligned16(Wq) || !aligned_to(w_scale, 4)) return QLORA_ERR_ALIGNMENT;
-  const Int8Layout l = int8_layout(M, K);
+  const Int8Layout l = int8_layout(M, K, N);
   if (!workspace || ws_bytes < l.total) return QLORA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -414,7 +414,7 @@ QLORA_API size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols);
  * and the product does not read past K.  codes are 16-byte aligned, X and Y as
  * their elements.
  * qlora_linear_int8_fwd quantizes X into the workspace and multiplies.
- * M, K, N >= 1, K <= 133144 (sums stay exact in 32 bits), M, N < 2^31 - 512;
+ * M, K, N >= 1, K <= 133144 (sums stay exact in 32 bits), M, N < 2^31 - 2^15;
  * otherwise QLORA_ERR_UNSUPPORTED.  Results do not depend on the order of
  * work.  workspace: at least qlora_int8_workspace_bytes bytes, the first 1024
  * filled with zeros once before its first use (status word and counters, which

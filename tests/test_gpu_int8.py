@@ -95,11 +95,11 @@ def test_product(M, K, N, dtype):
     ws = q.new_int8_workspace(M, K, N, DEV)
     ws[1024:].fill_(77)
     Y = torch.full((M, N), float("nan"), dtype=TYPES[dtype], device=DEV)
-    for _ in range(2):  # the second call finds the counters at zero again
+    for _ in range(2):
         assert q.qlora_matmul_int8(X, W, TYPES[dtype], workspace=ws, Y=Y) is Y
         assert q.qlora_check_status(ws) == 0
         check(Y, matmul_int8(xq, sx, wq, sw))
-    assert not ws[256:1024].any()
+    assert not ws[256:1024].any()  # the counters are back at zero
 
 
 @pytest.mark.parametrize("M,N", [(1, 256), (100, 128), (300, 136)])

@@ -1,5 +1,5 @@
-"""Host-side refusals of the 8-bit integer linear, and the run arithmetic of
-its few-token kernel (fake pointers are never read)."""
+"""Host-side refusals of the 8-bit integer linear (fake pointers are never
+read)."""
 
 import pytest
 import torch
@@ -29,7 +29,7 @@ def test_quantize_validation(L):
 
 def test_product_validation(L):
     need = L.qlora_int8_workspace_bytes(4, 30, 8)
-    assert need > 1024
+    assert need > 256
 
     def mm(x=FAKE, ldx=32, M=4, K=30, N=8, w=FAKE, ldw=32, y=FAKE, dt=BF16, ws=FAKE, nb=need):
         return L.qlora_matmul_int8(x, ldx, FAKE, M, K, N, w, ldw, FAKE, y, dt, ws, nb, None)
@@ -50,55 +50,6 @@ def test_workspace_bytes(L):
     assert L.qlora_int8_workspace_bytes(0, 8, 8) == 0 and L.qlora_int8_workspace_bytes(1, 133145, 8) == 0
     with pytest.raises(q.QloraError):
         q.new_int8_workspace(1, 0, 8, "cpu")
-
-
-def run_start(units, block, blocks):
-    return units * block // blocks
-
-
-@pytest.mark.parametrize("tiles,nkb", [(1, 1), (1, 64), (2, 3), (64, 64), (65, 32), (172, 64), (300, 1), (7, 1041)])
-def test_runs_cover_every_unit_once(tiles, nkb):
-    """The schedule of the few-token kernel: equal contiguous runs of (tile,
-    block of depth) units; every split tile is summed from one partial tile
-    per block that holds some of it, in that block's slot 0 (the run begins
-    inside the tile) or 1, and its counter is the block it begins in."""
-    units = tiles * nkb
-    blocks = min(148, -(-units // 4))
-    seen, slots, counters = set(), {}, {}
-    for b in range(blocks):
-        u, end = run_start(units, b, blocks), run_start(units, b + 1, blocks)
-        assert u < end
-        while u < end:
-            tile = u // nkb
-            t0, t1 = tile * nkb, (tile + 1) * nkb
-            stop = min(end, t1)
-            seen.update(range(u, stop))
-            if not (u == t0 and stop == t1):
-                slot = (b, int(u == t0))
-                assert slot not in slots
-                slots[slot] = tile
-                b0 = t0 * blocks // units
-                while b0 + 1 < blocks and run_start(units, b0 + 1, blocks) <= t0:
-                    b0 += 1
-                while b0 > 0 and run_start(units, b0, blocks) > t0:
-                    b0 -= 1
-                counters.setdefault(b0, tile)
-                assert counters[b0] == tile
-                # the summing block's list of partial tiles
-                parts = []
-                for c in range(b0, blocks):
-                    s = run_start(units, c, blocks)
-                    if s >= t1:
-                        break
-                    parts.append((c, int(s <= t0)))
-                assert slot in parts
-            u = stop
-    assert seen == set(range(units))
-    for tile in set(slots.values()):
-        t0, t1 = tile * nkb, (tile + 1) * nkb
-        holders = [(c, int(run_start(units, c, blocks) <= t0)) for c in range(blocks)
-                   if run_start(units, c, blocks) < t1 and run_start(units, c + 1, blocks) > t0]
-        assert all(slots.get(h) == tile for h in holders)
 
 
 def test_binding_refuses_cpu_tensors():
