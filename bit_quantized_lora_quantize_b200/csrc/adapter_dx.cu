@@ -136,14 +136,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int g = 0; g < 2; ++g) {
         const int64_t m = m0 + wm + 16 * i + 8 * h + (lane >> 2), k = k0 + wn + 32 * g + 8 * (lane & 3);
         if (m >= M || k >= K) continue;
-        const uint32_t keep = keep_bits(d, base + m * d.groups + k / 8);
+        const KeepGroup keep = keep_group(d, base + m * d.groups + k / 8);
         Raw8<__nv_bfloat16> x;
         x.w[0] = old[i][h][g].x; x.w[1] = old[i][h][g].y; x.w[2] = old[i][h][g].z; x.w[3] = old[i][h][g].w;
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float add = acc[i][4 * g + (e >> 1)][2 * h + (e & 1)];
-          v[e] = raw_f32(x, e) + (((keep >> e) & 1u) ? add : 0.0f);
+          v[e] = raw_f32(x, e) + (keep(e) ? add : 0.0f);
         }
         store_group_stream(reinterpret_cast<__nv_bfloat16*>(dX) + m * K + k, raw_from<__nv_bfloat16>(v));
       }

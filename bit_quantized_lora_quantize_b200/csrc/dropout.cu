@@ -48,11 +48,11 @@ __global__ void __launch_bounds__(kDropThreads)
   for (int u = 0; u < U; ++u) {
     const int64_t g = g0 + u * kDropThreads;
     if (g >= ngroups) return;
-    const uint32_t keep = keep_bits(d, base + g);
+    const KeepGroup keep = keep_group(d, base + g);
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      v[e] = drop_value(raw_f32(x[u], e), RES ? raw_f32(r[u], e) : 0.0f, (keep >> e) & 1u, d.gain);
+      v[e] = drop_value(raw_f32(x[u], e), RES ? raw_f32(r[u], e) : 0.0f, keep(e), d.gain);
     store_group_stream(Y + g * 8, raw_from<T>(v));
   }
 }
@@ -60,23 +60,23 @@ __global__ void __launch_bounds__(kDropThreads)
 // Ragged rows: one warp per 256 columns of a row, scalar accesses.
 template <typename T, bool RES>
 __global__ void __launch_bounds__(kDropThreads)
-    dropout_ragged_kernel(const T* __restrict__ X, const T* __restrict__ R, T* __restrict__ Y, int64_t cols,
+    dropout_ragged_kernel(const T* __restrict__ X, const T* __restrict__ R, T* __restrict__ Y, int cols,
                           int64_t chunks_per_row, int64_t nchunks, const DropArgs d) {
   const int lane = threadIdx.x & 31;
   const int64_t chunk = static_cast<int64_t>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5);
   if (chunk >= nchunks) return;
   const int64_t row = chunk / chunks_per_row;
-  const int64_t c0 = (chunk - row * chunks_per_row) * 256;
+  const int c0 = static_cast<int>(chunk - row * chunks_per_row) * 256;
   const int64_t at = row * cols;
   const Raw8<T> x = load_cols<false>(X + at, c0, cols, lane);
   Raw8<T> r;
   if (RES) r = load_cols<false>(R + at, c0, cols, lane);
-  const uint32_t keep = keep_bits_cols<false>(d, drop_base(d) + row * d.groups + c0 / 8, lane);
+  const KeepBits keep = keep_cols<false>(d, drop_base(d) + row * d.groups + c0 / 8, lane);
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    v[e] = drop_value(raw_f32(x, e), RES ? raw_f32(r, e) : 0.0f, (keep >> e) & 1u, d.gain);
-  store_cols<false>(Y + at, c0, cols, lane, v);
+    v[e] = drop_value(raw_f32(x, e), RES ? raw_f32(r, e) : 0.0f, keep(e), d.gain);
+  store_cols<false>(Y + at, c0, cols, lane, raw_from<T>(v));
 }
 
 template <typename T, bool RES>
@@ -96,7 +96,7 @@ cudaError_t launch_typed(const T* X, const T* R, T* Y, int64_t rows, int64_t col
     const int64_t per_row = (cols + 255) / 256, n = rows * per_row;
     const int64_t grid = (n + kDropThreads / 32 - 1) / (kDropThreads / 32);
     dropout_ragged_kernel<T, RES>
-        <<<static_cast<unsigned>(grid), kDropThreads, 0, stream>>>(X, R, Y, cols, per_row, n, d);
+        <<<static_cast<unsigned>(grid), kDropThreads, 0, stream>>>(X, R, Y, static_cast<int>(cols), per_row, n, d);
   }
   return cudaGetLastError();
 }

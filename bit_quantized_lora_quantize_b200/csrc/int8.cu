@@ -43,8 +43,8 @@ struct QuantArgs {
   const void* x;
   int8_t* codes;
   float* scale;
-  int64_t rows, cols, ld;
-  int wpr;
+  int64_t rows, ld;
+  int cols, wpr;
 };
 
 // Largest magnitude of a lane's eight values, as the bits of the float32:
@@ -111,12 +111,16 @@ struct RowScale {
       return;
     }
     float r[8], worst = 0.0f;
+    const F2 magic = f2_all(12582912.0f), inv2 = f2_all(inv), neg = f2_all(-s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = raw_f32(x, e), b = fmaf(v, inv, 12582912.0f);
-      c[e] = __float_as_uint(b);
-      r[e] = fmaf(12582912.0f - b, s, v);
-      worst = fmaxf(worst, fabsf(r[e]));
+    for (int p = 0; p < 4; ++p) {
+      const F2 v = raw_f2(x, p), b = fma2(v, inv2, magic);
+      const float2 bits = f2_get(b), rest = f2_get(fma2(add2(b, f2_all(-12582912.0f)), neg, v));
+      c[2 * p] = __float_as_uint(bits.x);
+      c[2 * p + 1] = __float_as_uint(bits.y);
+      r[2 * p] = rest.x;
+      r[2 * p + 1] = rest.y;
+      worst = fmaxf(worst, fmaxf(fabsf(rest.x), fabsf(rest.y)));
     }
     if (worst < half) return;
 #pragma unroll
@@ -126,14 +130,14 @@ struct RowScale {
 };
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store_codes(const QuantArgs& a, int64_t row, int64_t c0, int lane, const RowScale& rs,
+__device__ __forceinline__ void store_codes(const QuantArgs& a, int64_t row, int c0, int lane, const RowScale& rs,
                                             const Raw8<T>& x) {
-  const int64_t padded = (a.cols + 15) / 16 * 16;  // columns past the end hold 0
+  const int padded = (a.cols + 15) / 16 * 16;  // columns past the end hold 0
   int8_t* out = a.codes + row * a.ld;
   uint32_t k[8];
   rs.codes(x, k);
   if constexpr (VEC) {
-    const int64_t c = c0 + lane * 8;
+    const int c = c0 + lane * 8;
     if (c < padded)
       *reinterpret_cast<uint2*>(out + c) =
           make_uint2(prmt(prmt(k[0], k[1], 0x0040), prmt(k[2], k[3], 0x0040), 0x5410),
@@ -141,7 +145,7 @@ __device__ __forceinline__ void store_codes(const QuantArgs& a, int64_t row, int
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t c = c0 + lane + 32 * e;
+      const int c = c0 + lane + 32 * e;
       if (c < padded) out[c] = static_cast<int8_t>(k[e]);
     }
   }
@@ -170,12 +174,12 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const QuantArgs a) 
   uint32_t m = 0;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
+    const int c0 = (part + g * a.wpr) * 256;
     if (valid && c0 < a.cols) x[g] = load_cols<VEC>(xr, c0, a.cols, lane);
   }
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
+    const int c0 = (part + g * a.wpr) * 256;
     if (valid && c0 < a.cols) m = max(m, abs_max(x[g]));
   }
   m = row_max(m, red, warp, first, a.wpr);
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(1024) quantize_rows_kernel(const QuantArgs a) 
   if (part == 0 && lane == 0) a.scale[row] = rs.scale;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
+    const int c0 = (part + g * a.wpr) * 256;
     if (c0 < a.cols) store_codes<VEC>(a, row, c0, lane, rs, x[g]);
   }
 }
@@ -198,11 +202,11 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const QuantArg
   const int64_t row = blockIdx.x;
   const T* xr = static_cast<const T*>(a.x) + row * a.cols;
   uint32_t m = 0;
-  for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256)
+  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256)
     m = max(m, abs_max(load_cols<false>(xr, c0, a.cols, lane)));
   const RowScale rs(row_max(m, red, warp, 0, 32));
   if (threadIdx.x == 0) a.scale[row] = rs.scale;
-  for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256)
+  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256)
     store_codes<false>(a, row, c0, lane, rs, load_cols<false>(xr, c0, a.cols, lane));
 }
 
@@ -814,7 +818,7 @@ qlora_status qlora_quantize_int8(const void* X, int64_t rows, int64_t cols, int3
   if (sh != QLORA_OK) return sh;
   if (bad_stride(ld, cols)) return QLORA_ERR_INVALID_ARG;
   if (!aligned_to(X, dtype_bytes(dtype)) || !aligned16(codes) || !aligned_to(scale, 4)) return QLORA_ERR_ALIGNMENT;
-  const QuantArgs a{X, codes, scale, rows, cols, ld, 1};
+  const QuantArgs a{X, codes, scale, rows, ld, static_cast<int>(cols), 1};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(st, "quantize_int8", 1);
   const cudaError_t e = launch_quantize_int8(dtype, a, st);
@@ -864,7 +868,7 @@ qlora_status qlora_linear_int8_fwd(const void* X, int64_t M, int64_t K, int64_t 
   float* scale = reinterpret_cast<float*>(ws + l.scale);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(st, "linear_int8_fwd", 2);
-  cudaError_t e = launch_quantize_int8(dtype, QuantArgs{X, codes, scale, M, K, padded_depth(K), 1}, st);
+  cudaError_t e = launch_quantize_int8(dtype, QuantArgs{X, codes, scale, M, padded_depth(K), static_cast<int>(K), 1}, st);
   if (e == cudaSuccess)
     e = launch_matmul_int8(dtype, codes, padded_depth(K), scale, M, K, N, Wq, ldw, w_scale, Y, ws, true, st);
   prof.done();

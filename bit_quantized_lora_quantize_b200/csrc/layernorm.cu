@@ -15,16 +15,17 @@
 // type, which is what the backward pass reads.
 //
 // Forward: `wpr` warps share a row, 256 columns per warp and step, so that a
-// row of up to 32768 columns stays in registers; many rows per SM hide each
+// row of up to 16384 columns stays in registers; many rows per SM hide each
 // other's reduction.  With few rows each gets as many warps as its columns
 // allow instead (one step per warp).  Longer rows are read three times.
 //
 // Backward: one persistent block per SM walks over the rows.  A ring of
 // stages in shared memory, filled by bulk copies, keeps whole rows of dY and Z
-// in flight while earlier ones are reduced; each thread carries the sums of
-// dweight and dbias for its columns in registers across all rows of the block.
-// The blocks' partial sums are added by a second, small kernel in a fixed
-// order, so results are the same from run to run.
+// in flight; each thread carries the sums of dweight and dbias for its columns
+// in registers across all rows of the block.  The blocks' partial sums are
+// added by a second, small kernel in a fixed order, so results are the same
+// from run to run.  Rows of over 8192 columns take one block each and a second
+// pass for the parameters.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -42,8 +43,10 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kFwdMaxGroups = 4;         // steps of 256 columns a warp holds in the forward
+constexpr int kFwdWarps = 16;            // warps of a forward block (32 with one step each)
 constexpr int kBwdGroups = 2;            // the same in the backward
-constexpr int kBwdWarps = 16;
+constexpr int kBwdWarps = 16;            // that compute; one more feeds the ring
+constexpr int kBwdThreads = (kBwdWarps + 1) * 32;
 constexpr int kBwdCols = kBwdWarps * 256 * kBwdGroups;  // widest row of the ring kernel
 constexpr int kBwdMaxBlocks = 160;       // partial sums in the workspace
 constexpr int kRingBytes = 200 * 1024;
@@ -69,7 +72,7 @@ __device__ __forceinline__ float row_sum(float v, float* buf, int warp, int firs
 }
 
 template <bool VEC>
-__device__ __forceinline__ bool col_in(int64_t c0, int lane, int e, int64_t cols) {
+__device__ __forceinline__ bool col_in(int c0, int lane, int e, int cols) {
   return c0 + warp_col<VEC>(lane, e) < cols;
 }
 
@@ -82,7 +85,8 @@ struct LnFwdArgs {
   void* y;
   float* mean;
   float* rstd;
-  int64_t rows, cols;
+  int64_t rows;
+  int cols;
   float eps, inv_n;
   int wpr;
   DropArgs drop;
@@ -91,70 +95,93 @@ struct LnFwdArgs {
 // Values of one lane's eight columns after the residual dropout, rounded to
 // T and stored to Z.
 template <typename T, bool VEC>
-__device__ __forceinline__ Raw8<T> add_dropped(const LnFwdArgs& a, int64_t row, int64_t c0, int lane, uint64_t base,
-                                               const Raw8<T>& x) {
-  const int64_t at = row * a.cols;
-  const Raw8<T> r = load_cols<VEC>(static_cast<const T*>(a.residual) + at, c0, a.cols, lane);
-  const uint32_t keep = keep_bits_cols<VEC>(a.drop, base + row * a.drop.groups + c0 / 8, lane);
+__device__ __forceinline__ Raw8<T> add_dropped(const LnFwdArgs& a, int64_t row, int c0, int lane, uint64_t base,
+                                               const Raw8<T>& x, const Raw8<T>& r) {
+  const auto keep = keep_cols<VEC>(a.drop, base + row * a.drop.groups + c0 / 8, lane);
   float v[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    v[e] = ((keep >> e) & 1u) ? fmaf(raw_f32(x, e), a.drop.gain, raw_f32(r, e)) : raw_f32(r, e);
-  store_cols<VEC>(static_cast<T*>(a.z) + at, c0, a.cols, lane, v);
-  return raw_from<T>(v);
+  for (int e = 0; e < 8; ++e) v[e] = keep(e) ? fmaf(raw_f32(x, e), a.drop.gain, raw_f32(r, e)) : raw_f32(r, e);
+  const Raw8<T> z = raw_from<T>(v);
+  store_cols<VEC>(static_cast<T*>(a.z) + row * a.cols, c0, a.cols, lane, z);
+  return z;
+}
+
+// Sum of a lane's eight values (zeros past the end), and of their squared
+// distances from the mean.
+template <typename T>
+__device__ __forceinline__ float group_sum(const Raw8<T>& x) {
+  return f2_sum(add2(add2(raw_f2(x, 0), raw_f2(x, 1)), add2(raw_f2(x, 2), raw_f2(x, 3))));
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ float group_spread(const Raw8<T>& x, float mean, int c0, int lane, int cols) {
+  const F2 m = f2_all(-mean);
+  F2 q = 0;
+  if (c0 + 256 <= cols) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const F2 d = add2(raw_f2(x, p), m);
+      q = fma2(d, d, q);
+    }
+    return f2_sum(q);
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float d = raw_f32(x, e) - mean;
+    if (col_in<VEC>(c0, lane, e, cols)) s = fmaf(d, d, s);
+  }
+  return s;
 }
 
 template <typename T, typename W, bool VEC>
-__device__ __forceinline__ void normalise(const LnFwdArgs& a, int64_t row, int64_t c0, int lane, float mean, float rstd,
+__device__ __forceinline__ void normalise(const LnFwdArgs& a, int64_t row, int c0, int lane, float mean, float rstd,
                                           const Raw8<T>& x) {
-  Raw8<W> w, b;
-  if (a.w) w = load_cols<VEC>(static_cast<const W*>(a.w), c0, a.cols, lane);
-  if (a.b) b = load_cols<VEC>(static_cast<const W*>(a.b), c0, a.cols, lane);
-  float v[8];
+  const Raw8<W> w = a.w ? load_cols<VEC>(static_cast<const W*>(a.w), c0, a.cols, lane) : raw_ones<W>();
+  const Raw8<W> b = a.b ? load_cols<VEC>(static_cast<const W*>(a.b), c0, a.cols, lane) : raw_zero<W>();
+  const F2 m = f2_all(-mean), r = f2_all(rstd);
+  F2 v[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    v[e] = fmaf((raw_f32(x, e) - mean) * rstd, a.w ? raw_f32(w, e) : 1.0f, a.b ? raw_f32(b, e) : 0.0f);
-  store_cols<VEC>(static_cast<T*>(a.y) + row * a.cols, c0, a.cols, lane, v);
+  for (int p = 0; p < 4; ++p) {
+    const F2 h = mul2(add2(raw_f2(x, p), m), r);
+    v[p] = fma2(h, raw_f2(w, p), raw_f2(b, p));
+  }
+  store_cols<VEC>(static_cast<T*>(a.y) + row * a.cols, c0, a.cols, lane, raw_from_pairs<T>(v));
 }
 
 template <typename T, typename W, int G, bool VEC, bool FUSED>
-__global__ void __launch_bounds__(1024) ln_fwd_kernel(const LnFwdArgs a) {
+__global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kernel(const LnFwdArgs a) {
   __shared__ float red[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = warp % a.wpr, first = warp - part;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32 / a.wpr) + warp / a.wpr;
   const bool valid = row < a.rows;
   const T* xr = static_cast<const T*>(a.x) + row * a.cols;
-  Raw8<T> x[G];
+  const T* rr = static_cast<const T*>(a.residual) + row * a.cols;
+  Raw8<T> x[G], r[FUSED ? G : 1];
   float s = 0.0f;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
-    if (valid && c0 < a.cols) x[g] = load_cols<VEC>(xr, c0, a.cols, lane);
+    const int c0 = (part + g * a.wpr) * 256;
+    if (valid && c0 < a.cols) {
+      x[g] = load_cols<VEC>(xr, c0, a.cols, lane);
+      if constexpr (FUSED) r[g] = load_cols<VEC>(rr, c0, a.cols, lane);
+    }
   }
   const uint64_t base = FUSED ? drop_base(a.drop) : 0;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
+    const int c0 = (part + g * a.wpr) * 256;
     if (valid && c0 < a.cols) {
-      if (FUSED) x[g] = add_dropped<T, VEC>(a, row, c0, lane, base, x[g]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (col_in<VEC>(c0, lane, e, a.cols)) s += raw_f32(x[g], e);
+      if constexpr (FUSED) x[g] = add_dropped<T, VEC>(a, row, c0, lane, base, x[g], r[g]);
+      s += group_sum(x[g]);
     }
   }
   const float mean = row_sum(s, red[0], warp, first, a.wpr) * a.inv_n;
   float q = 0.0f;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
-    if (valid && c0 < a.cols) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = raw_f32(x[g], e) - mean;
-        if (col_in<VEC>(c0, lane, e, a.cols)) q = fmaf(d, d, q);
-      }
-    }
+    const int c0 = (part + g * a.wpr) * 256;
+    if (valid && c0 < a.cols) q += group_spread<VEC>(x[g], mean, c0, lane, a.cols);
   }
   const float rstd = 1.0f / sqrtf(row_sum(q, red[1], warp, first, a.wpr) * a.inv_n + a.eps);
   if (!valid) return;
@@ -164,7 +191,7 @@ __global__ void __launch_bounds__(1024) ln_fwd_kernel(const LnFwdArgs a) {
   }
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
+    const int c0 = (part + g * a.wpr) * 256;
     if (c0 < a.cols) normalise<T, W, VEC>(a, row, c0, lane, mean, rstd, x[g]);
   }
 }
@@ -179,31 +206,25 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(const LnFwdArgs a) {
   const T* xr = static_cast<const T*>(a.x) + row * a.cols;
   const uint64_t base = FUSED ? drop_base(a.drop) : 0;
   float s = 0.0f;
-  for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256) {
+  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
     Raw8<T> x = load_cols<false>(xr, c0, a.cols, lane);
-    if (FUSED) x = add_dropped<T, false>(a, row, c0, lane, base, x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (col_in<false>(c0, lane, e, a.cols)) s += raw_f32(x, e);
+    if constexpr (FUSED)
+      x = add_dropped<T, false>(a, row, c0, lane, base, x,
+                                load_cols<false>(static_cast<const T*>(a.residual) + row * a.cols, c0, a.cols, lane));
+    s += group_sum(x);
   }
   const float mean = row_sum(s, red[0], warp, 0, 32) * a.inv_n;
   // Each thread reads back only what it stored itself.
   const T* zr = FUSED ? static_cast<const T*>(a.z) + row * a.cols : xr;
   float q = 0.0f;
-  for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256) {
-    const Raw8<T> x = load_cols<false>(zr, c0, a.cols, lane);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float d = raw_f32(x, e) - mean;
-      if (col_in<false>(c0, lane, e, a.cols)) q = fmaf(d, d, q);
-    }
-  }
+  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256)
+    q += group_spread<false>(load_cols<false>(zr, c0, a.cols, lane), mean, c0, lane, a.cols);
   const float rstd = 1.0f / sqrtf(row_sum(q, red[1], warp, 0, 32) * a.inv_n + a.eps);
   if (threadIdx.x == 0) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
   }
-  for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256)
+  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256)
     normalise<T, W, false>(a, row, c0, lane, mean, rstd, load_cols<false>(zr, c0, a.cols, lane));
 }
 
@@ -218,11 +239,14 @@ struct LnBwdArgs {
   void* dx;          // fused form: dropout(dz total); else dz itself
   void* dres;        // fused form: dz total
   float* part;       // [blocks][2][cols] sums of dweight and dbias, or null
-  int64_t rows, cols;
+  float* dw;         // where a single block leaves the sums
+  float* db;
+  int64_t rows;
+  int cols;
   float inv_n;
   int wpr;
   int stages;
-  uint32_t tensor_bytes;  // one tensor's rows in a stage
+  uint32_t tensor_bytes;  // room for one tensor's rows in a stage
   int* status;
   uint64_t wait_ns;
   DropArgs drop;
@@ -235,223 +259,377 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-__device__ __forceinline__ float grad_value(float dy, float h, float w, float s1, float s2, float rstd) {
-  return rstd * (fmaf(dy, w, -s1) - h * s2);
+// dz = rstd (dy w - s1 - h s2) [+ the gradient past the norm], four pairs of it
+// to memory, and dropout(dz) in the fused form.
+template <typename T, bool VEC, bool FUSED>
+__device__ __forceinline__ void store_grad(const LnBwdArgs& a, int64_t row, int64_t at, int c0, int lane, uint64_t base,
+                                           const F2 (&v)[4]) {
+  if constexpr (!FUSED) {
+    store_cols<VEC>(static_cast<T*>(a.dx) + at, c0, a.cols, lane, raw_from_pairs<T>(v));
+  } else {
+    store_cols<VEC>(static_cast<T*>(a.dres) + at, c0, a.cols, lane, raw_from_pairs<T>(v));
+    const auto keep = keep_cols<VEC>(a.drop, base + row * a.drop.groups + c0 / 8, lane);
+    float f[8];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float2 d = f2_get(mul2(v[p], f2_all(a.drop.gain)));
+      f[2 * p] = keep(2 * p) ? d.x : 0.0f;
+      f[2 * p + 1] = keep(2 * p + 1) ? d.y : 0.0f;
+    }
+    store_cols<VEC>(static_cast<T*>(a.dx) + at, c0, a.cols, lane, raw_from<T>(f));
+  }
 }
 
-template <typename T, bool VEC, bool FUSED>
-__device__ __forceinline__ void store_grad(const LnBwdArgs& a, int64_t row, int64_t c0, int lane, uint64_t base,
-                                           float (&v)[8]) {
-  const int64_t at = row * a.cols;
-  if (!FUSED) {
-    store_cols<VEC>(static_cast<T*>(a.dx) + at, c0, a.cols, lane, v);
+// A lane's eight float32 values to row[c0 ..]; `row` is aligned for vectors when
+// VEC and the columns a multiple of eight.
+template <bool VEC>
+__device__ __forceinline__ void store_pairs(float* row, int c0, int cols, int lane, const F2 (&v)[4]) {
+  if (VEC && aligned_group(row)) {
+    const int c = c0 + lane * 8;
+    if (c < cols) store_group(row + c, raw_from_pairs<float>(v));
     return;
   }
-  store_cols<VEC>(static_cast<T*>(a.dres) + at, c0, a.cols, lane, v);
-  const uint32_t keep = keep_bits_cols<VEC>(a.drop, base + row * a.drop.groups + c0 / 8, lane);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = ((keep >> e) & 1u) ? v[e] * a.drop.gain : 0.0f;
-  store_cols<VEC>(static_cast<T*>(a.dx) + at, c0, a.cols, lane, v);
+  for (int p = 0; p < 4; ++p) {
+    const float2 d = f2_get(v[p]);
+    const int c = c0 + warp_col<VEC>(lane, 2 * p), e = c0 + warp_col<VEC>(lane, 2 * p + 1);
+    if (c < cols) row[c] = d.x;
+    if (e < cols) row[e] = d.y;
+  }
 }
 
-// RING: aligned rows through the ring of bulk copies; otherwise ragged rows
-// by scalar loads.
-template <typename T, typename W, bool RING, bool FUSED>
-__global__ void __launch_bounds__(kBwdWarps * 32, 1) ln_bwd_kernel(const LnBwdArgs a) {
+// Ring of bulk copies over one tensor's rows.  Rows need not be aligned: a
+// copy covers the 16-byte blocks around a stage's rows, except that it stays
+// inside the tensor; the few elements this leaves out at the tensor's two ends
+// are stored by the issuing thread.
+template <typename T>
+struct RowRing {
+  const T* base;
+  int64_t total;  // elements
+  __device__ __forceinline__ uint32_t shift(int64_t at) const {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base + at) & 15u);
+  }
+  // Bytes that load() will copy for elements [at, at + n).
+  __device__ __forceinline__ void span(int64_t at, int64_t n, uintptr_t& lo, uintptr_t& hi) const {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(base), e = reinterpret_cast<uintptr_t>(base + total);
+    lo = reinterpret_cast<uintptr_t>(base + at) & ~uintptr_t(15);
+    hi = (reinterpret_cast<uintptr_t>(base + at + n) + 15) & ~uintptr_t(15);
+    if (lo < b) lo = (b + 15) & ~uintptr_t(15);
+    if (hi > e) hi = e & ~uintptr_t(15);
+    if (hi < lo) hi = lo;
+  }
+  // Element `at` lands at dst + shift(at).
+  __device__ __forceinline__ void load(uint8_t* dst, int64_t at, int64_t n, uint64_t* bar) const {
+    uintptr_t lo, hi;
+    span(at, n, lo, hi);
+    const uintptr_t from = reinterpret_cast<uintptr_t>(base + at) & ~uintptr_t(15);
+    if (hi > lo)
+      bulk_load(dst + (lo - from), reinterpret_cast<const void*>(lo), static_cast<uint32_t>(hi - lo), bar);
+  }
+  // The elements that load() leaves out, at most seven at each end of the tensor.
+  __device__ __forceinline__ void ends(uint8_t* dst, int64_t at, int64_t n) const {
+    uintptr_t lo, hi;
+    span(at, n, lo, hi);
+    const uintptr_t b = reinterpret_cast<uintptr_t>(base + at), e = reinterpret_cast<uintptr_t>(base + at + n);
+    T* to = reinterpret_cast<T*>(dst + shift(at));
+    if (lo > b) {
+      const int64_t head = min(n, static_cast<int64_t>((lo - b) / sizeof(T)));
+      for (int64_t i = 0; i < head; ++i) to[i] = base[at + i];
+    }
+    if (hi < e) {
+      const int64_t tail = min(n, static_cast<int64_t>((e - hi) / sizeof(T)));
+      for (int64_t i = n - tail; i < n; ++i) to[i] = base[at + i];
+    }
+  }
+};
+
+// Two sums over the wpr warps of a row from the block's per-warp values.
+__device__ __forceinline__ float2 row_pair(const float (*red)[2], int first, int wpr) {
+  const float2 one = *reinterpret_cast<const float2*>(red[first]);
+  if (wpr == 1) return one;
+  F2 s = 0;
+#pragma unroll 8
+  for (int k = 0; k < wpr; k += 2) {
+    const float4 v = *reinterpret_cast<const float4*>(red[first + k]);
+    s = add2(s, add2(f2(v.x, v.y), f2(v.z, v.w)));
+  }
+  return f2_get(s);
+}
+
+// Each step of a block: its sums over step i + 1, then the gradients of step
+// i, whose sums the barrier at the end of the previous step made visible.  So
+// one barrier per step, with independent work on both sides of it.  A warp of
+// its own feeds the ring: its address arithmetic would otherwise hold up the
+// barrier of every step (2 us a step before, whatever the columns).
+template <typename T, typename W, bool VEC, bool FUSED>
+__global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs a) {
   constexpr int G = kBwdGroups;
-  constexpr bool VEC = RING;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float red[2][2][kBwdWarps];
-  __shared__ __align__(8) uint64_t full[kMaxStages];
+  __shared__ __align__(16) float red[2][kBwdWarps][2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
+  __shared__ float2 row_stats[kMaxStages][kBwdWarps];  // mean and rstd of a stage's rows
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = warp % a.wpr, first = warp - part, slot = warp / a.wpr;
   const int rpi = kBwdWarps / a.wpr;  // rows per step of the block
   const int64_t steps = (a.rows + rpi - 1) / rpi;
-  const int64_t mine = (steps - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  const int mine = static_cast<int>((steps - blockIdx.x + gridDim.x - 1) / gridDim.x);
   const bool has_dz = FUSED && a.dz;
   const int tensors = has_dz ? 3 : 2;
   const uint32_t stage_bytes = a.tensor_bytes * tensors;
-  int64_t issued = 0;  // by thread 0
+  const RowRing<T> ring_of[3] = {{static_cast<const T*>(a.dy), a.rows * a.cols},
+                                 {static_cast<const T*>(a.z), a.rows * a.cols},
+                                 {static_cast<const T*>(a.dz), a.rows * a.cols}};
 
-  auto issue = [&](int64_t i) {
-    ++issued;
-    const int s = static_cast<int>(i % a.stages);
-    const int64_t row = (blockIdx.x + i * gridDim.x) * rpi;
-    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(rpi), a.rows - row) * a.cols * sizeof(T));
-    uint8_t* dst = ring + s * stage_bytes;
-    const int64_t at = row * a.cols;
-    mbar_arrive_expect_tx(&full[s], bytes * tensors);
-    bulk_load(dst, static_cast<const T*>(a.dy) + at, bytes, &full[s]);
-    bulk_load(dst + a.tensor_bytes, static_cast<const T*>(a.z) + at, bytes, &full[s]);
-    if (has_dz) bulk_load(dst + 2 * a.tensor_bytes, static_cast<const T*>(a.dz) + at, bytes, &full[s]);
-  };
-
-  if (RING) {
-    if (threadIdx.x == 0) {
-      for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
-      abort_flag = 0;
-      fence_mbarrier_init();
-      for (int64_t i = 0; i < min(mine, static_cast<int64_t>(a.stages)); ++i) issue(i);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    __syncthreads();
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  if (warp == kBwdWarps) {
+    const WaitCtx ctx{&abort_flag, a.status, 42, a.wait_ns};
+    // Lane l looks after the statistics of a step's row l, one step ahead.
+    float2 ahead;
+    const auto look = [&](int i) {
+      const int64_t row = (static_cast<int64_t>(i) * gridDim.x + blockIdx.x) * rpi + lane;
+      const bool in = lane < rpi && row < a.rows;
+      ahead.x = in ? __ldg(a.mean + row) : 0.0f;
+      ahead.y = in ? __ldg(a.rstd + row) : 0.0f;
+    };
+    look(0);
+    int issued = 0;
+    for (; issued < mine; ++issued) {
+      const int s = issued % a.stages;
+      if (!__all_sync(kAll, mbar_wait(&empty[s], static_cast<uint32_t>((issued / a.stages) & 1) ^ 1, ctx))) break;
+      const int64_t row = (static_cast<int64_t>(issued) * gridDim.x + blockIdx.x) * rpi, at = row * a.cols;
+      const int64_t n = min(static_cast<int64_t>(rpi), a.rows - row) * a.cols;
+      uint8_t* dst = ring + s * stage_bytes;
+      if (lane < rpi) row_stats[s][lane] = ahead;
+      __syncwarp();
+      if (lane == 0) {
+        // The arrival publishes the statistics and the ends to whoever waits
+        // for the stage.
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          if (t < tensors) {
+            if (!VEC) ring_of[t].ends(dst + t * a.tensor_bytes, at, n);
+            uintptr_t lo, hi;
+            ring_of[t].span(at, n, lo, hi);
+            bytes += static_cast<uint32_t>(hi - lo);
+          }
+        }
+        mbar_arrive_expect_tx(&full[s], bytes);
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          if (t < tensors) ring_of[t].load(dst + t * a.tensor_bytes, at, n, &full[s]);
+      }
+      look(issued + 1);
+    }
+    if (abort_flag && lane == 0)  // copies still in flight must land before the block leaves
+      for (int i = max(0, issued - a.stages); i < issued; ++i)
+        mbar_drain(&full[i % a.stages], static_cast<uint32_t>((i / a.stages) & 1));
+    return;
   }
   const WaitCtx ctx{&abort_flag, a.status, 41, a.wait_ns};
   const uint64_t base = FUSED ? drop_base(a.drop) : 0;
 
-  Raw8<W> w[G];
-  float aw[G][8], ab[G][8];
+  F2 w[G][4], aw[G][4], ab[G][4];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
-    if (a.w && c0 < a.cols) w[g] = load_cols<VEC>(static_cast<const W*>(a.w), c0, a.cols, lane);
+    const int c0 = (part + g * a.wpr) * 256;
+    const Raw8<W> raw = a.w ? load_cols<VEC>(static_cast<const W*>(a.w), c0, a.cols, lane) : raw_ones<W>();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) aw[g][e] = ab[g][e] = 0.0f;
-  }
-  float mean_n = 0.0f, rstd_n = 0.0f;
-  {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * rpi + slot;
-    if (mine > 0 && row < a.rows) {
-      mean_n = __ldg(a.mean + row);
-      rstd_n = __ldg(a.rstd + row);
+    for (int p = 0; p < 4; ++p) {
+      w[g][p] = raw_f2(raw, p);
+      aw[g][p] = ab[g][p] = 0;
     }
   }
-
-  for (int64_t i = 0; i < mine; ++i) {
-    const int64_t row = (blockIdx.x + i * gridDim.x) * rpi + slot;
-    const bool valid = row < a.rows;
-    const float mean = mean_n, rstd = rstd_n;
-    const int64_t row_n = row + static_cast<int64_t>(gridDim.x) * rpi;
-    if (i + 1 < mine && row_n < a.rows) {
-      mean_n = __ldg(a.mean + row_n);
-      rstd_n = __ldg(a.rstd + row_n);
-    }
-    const int s = RING ? static_cast<int>(i % a.stages) : 0;
-    if (RING) mbar_wait(&full[s], static_cast<uint32_t>((i / a.stages) & 1), ctx);
-    const T* dyr = RING ? reinterpret_cast<const T*>(ring + s * stage_bytes) + slot * a.cols
-                        : static_cast<const T*>(a.dy) + row * a.cols;
-    const T* zr = RING ? reinterpret_cast<const T*>(ring + s * stage_bytes + a.tensor_bytes) + slot * a.cols
-                       : static_cast<const T*>(a.z) + row * a.cols;
-    const T* dzr = RING ? reinterpret_cast<const T*>(ring + s * stage_bytes + 2 * a.tensor_bytes) + slot * a.cols
-                        : static_cast<const T*>(a.dz) + row * a.cols;
-    Raw8<T> dy[G], z[G], dz[G];
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
-      if (valid && c0 < a.cols) {
-        dy[g] = load_cols<VEC>(dyr, c0, a.cols, lane);
-        z[g] = load_cols<VEC>(zr, c0, a.cols, lane);
-        if (has_dz) dz[g] = load_cols<VEC>(dzr, c0, a.cols, lane);
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
-      if (valid && c0 < a.cols) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          // columns past the end hold dY = 0 and add nothing
-          const float d = raw_f32(dy[g], e);
-          const float h = col_in<VEC>(c0, lane, e, a.cols) ? (raw_f32(z[g], e) - mean) * rstd : 0.0f;
-          const float gr = a.w ? d * raw_f32(w[g], e) : d;
-          s1 += gr;
-          s2 = fmaf(gr, h, s2);
-          aw[g][e] = fmaf(d, h, aw[g][e]);
-          ab[g][e] += d;
-        }
-      }
-    }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    float(*rb)[kBwdWarps] = red[i & 1];
-    if (lane == 0) {
-      rb[0][warp] = s1;
-      rb[1][warp] = s2;
-    }
-    __syncthreads();  // sums visible; the stage has been read by everyone
-    if (RING && threadIdx.x == 0 && i + a.stages < mine && !abort_flag) issue(i + a.stages);
-    s1 = s2 = 0.0f;
-    for (int k = 0; k < a.wpr; ++k) {
-      s1 += rb[0][first + k];
-      s2 += rb[1][first + k];
-    }
-    s1 *= a.inv_n;
-    s2 *= a.inv_n;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
-      if (valid && c0 < a.cols) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float h = (raw_f32(z[g], e) - mean) * rstd;
-          v[e] = grad_value(raw_f32(dy[g], e), h, a.w ? raw_f32(w[g], e) : 1.0f, s1, s2, rstd);
-          if (has_dz) v[e] += raw_f32(dz[g], e);
-        }
-        store_grad<T, VEC, FUSED>(a, row, c0, lane, base, v);
-      }
-    }
-  }
-
-  if (RING && abort_flag) {
-    // Copies still in flight must land before the block leaves.
-    if (threadIdx.x == 0)
-      for (int64_t i = max(int64_t(0), issued - a.stages); i < issued; ++i)
-        mbar_drain(&full[i % a.stages], static_cast<uint32_t>((i / a.stages) & 1));
-    __syncthreads();
-  }
-  if (!a.part) return;
-  // Add the row slots' sums in shared memory, slot by slot in order.
-  float* pw = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-  float* acc = reinterpret_cast<float*>(ring);
-  __syncthreads();
-  for (int k = 0; k < rpi; ++k) {
-    if (slot == k) {
+  // This step's row and the next one's: where it is, its statistics and its
+  // place in the ring.
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * rpi, stride_at = stride * a.cols;
+  struct Row {
+    int64_t row, at;  // row number, first element
+    const uint8_t* stage;
+    float mean, rstd;
+  };
+  // The row's columns of tensor t in the ring (a stage starts at its first row).
+  const auto row_in = [&](const Row& r, int t) {
+    const uint32_t shift = VEC ? 0u : ring_of[t].shift(r.at - static_cast<int64_t>(slot) * a.cols);
+    return reinterpret_cast<const T*>(r.stage + t * a.tensor_bytes + shift) + slot * a.cols;
+  };
+  const auto sums = [&](Row& r, int s, float(*out)[2]) {
+    F2 s1 = 0, s2 = 0;
+    const float2 st = row_stats[s][slot];
+    r.mean = st.x;
+    r.rstd = st.y;
+    if (r.row < a.rows) {
+      const T* dyr = row_in(r, 0);
+      const T* zr = row_in(r, 1);
+      const F2 nm = f2_all(-r.mean), rs = f2_all(r.rstd);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const int64_t c0 = static_cast<int64_t>(part + g * a.wpr) * 256;
+        const int c0 = (part + g * a.wpr) * 256;
+        if (c0 < a.cols) {
+          // columns past the end hold dY = 0 and add nothing
+          const Raw8<T> dy = load_cols<VEC>(dyr, c0, a.cols, lane), z = load_cols<VEC>(zr, c0, a.cols, lane);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t c = c0 + warp_col<VEC>(lane, e);
-          if (c < a.cols) {
-            const float vw = k ? acc[c] + aw[g][e] : aw[g][e];
-            const float vb = k ? acc[a.cols + c] + ab[g][e] : ab[g][e];
-            if (k + 1 < rpi) {
-              acc[c] = vw;
-              acc[a.cols + c] = vb;
-            } else {
-              pw[c] = vw;
-              pw[a.cols + c] = vb;
-            }
+          for (int p = 0; p < 4; ++p) {
+            const F2 d = raw_f2(dy, p), h = mul2(add2(raw_f2(z, p), nm), rs), gr = mul2(d, w[g][p]);
+            aw[g][p] = fma2(d, h, aw[g][p]);
+            ab[g][p] = add2(ab[g][p], d);
+            s1 = add2(s1, gr);
+            s2 = fma2(gr, h, s2);
           }
         }
       }
     }
-    if (k + 1 < rpi) __syncthreads();
+    // Half of the warp goes on with the first sum, half with the second.
+    const float u = f2_sum(s1), v = f2_sum(s2);
+    const bool upper = lane & 16;
+    float keep = upper ? v : u;
+    keep += __shfl_xor_sync(kAll, upper ? u : v, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) keep += __shfl_xor_sync(kAll, keep, o);
+    if ((lane & 15) == 0) out[warp][lane >> 4] = keep;
+  };
+
+  Row cur, next;
+  next.row = static_cast<int64_t>(blockIdx.x) * rpi + slot;
+  next.at = next.row * a.cols;
+  next.stage = ring;
+  int s = 0;             // stage of `next`
+  uint32_t parity = 0;
+  const auto advance = [&] {
+    next.row += stride;
+    next.at += stride_at;
+    if (++s == a.stages) {
+      s = 0;
+      parity ^= 1;
+    }
+    next.stage = ring + s * stage_bytes;
+  };
+  // The computing warps' own barrier.
+  const auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kBwdWarps * 32) : "memory"); };
+  mbar_wait(&full[0], 0, ctx);  // every block has a step
+  sums(next, 0, red[0]);
+  cur = next;
+  advance();
+  sync();
+  int s_cur = 0;
+  for (int i = 0; i < mine; ++i) {
+    if (i + 1 < mine) {
+      mbar_wait(&full[s], parity, ctx);
+      sums(next, s, red[(i + 1) & 1]);
+    }
+    if (cur.row < a.rows) {
+      const float2 sum = row_pair(red[i & 1], first, a.wpr);
+      const F2 nm = f2_all(-cur.mean), rs = f2_all(cur.rstd);
+      const F2 s1 = f2_all(-sum.x * a.inv_n), s2 = f2_all(-sum.y * a.inv_n);
+      const T* dyr = row_in(cur, 0);
+      const T* zr = row_in(cur, 1);
+      const T* dzr = row_in(cur, 2);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int c0 = (part + g * a.wpr) * 256;
+        if (c0 < a.cols) {
+          const Raw8<T> dy = load_cols<VEC>(dyr, c0, a.cols, lane), z = load_cols<VEC>(zr, c0, a.cols, lane);
+          F2 v[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const F2 h = mul2(add2(raw_f2(z, p), nm), rs);
+            v[p] = mul2(fma2(h, s2, fma2(raw_f2(dy, p), w[g][p], s1)), rs);
+          }
+          if (has_dz) {
+            const Raw8<T> dz = load_cols<VEC>(dzr, c0, a.cols, lane);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) v[p] = add2(v[p], raw_f2(dz, p));
+          }
+          store_grad<T, VEC, FUSED>(a, cur.row, cur.at, c0, lane, base, v);
+        }
+      }
+    }
+    cur = next;
+    advance();
+    sync();  // step i + 1's sums are visible, stage i has been read
+    if (threadIdx.x == 0) mbar_arrive(&empty[s_cur]);
+    if (++s_cur == a.stages) s_cur = 0;
+  }
+  griddep_launch_dependents();
+
+  if (!a.part && !a.dw && !a.db) return;
+  float* pw = a.part ? a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols : a.dw;
+  float* pb = a.part ? pw + a.cols : a.db;
+  if (rpi == 1) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int c0 = (part + g * a.wpr) * 256;
+      if (pw) store_pairs<VEC>(pw, c0, a.cols, lane, aw[g]);
+      if (pb) store_pairs<VEC>(pb, c0, a.cols, lane, ab[g]);
+    }
+    return;
+  }
+  // The row slots' sums, added in slot order: [slot][dweight, dbias][column].
+  float* acc = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int c0 = (part + g * a.wpr) * 256;
+    store_pairs<VEC>(acc + (slot * 2) * a.cols, c0, a.cols, lane, aw[g]);
+    store_pairs<VEC>(acc + (slot * 2 + 1) * a.cols, c0, a.cols, lane, ab[g]);
+  }
+  sync();
+  for (int c = threadIdx.x; c < 2 * a.cols; c += kBwdWarps * 32) {
+    float sum = 0.0f;
+    for (int k = 0; k < rpi; ++k) sum += acc[k * 2 * a.cols + c];
+    if (c < a.cols) {
+      if (pw) pw[c] = sum;
+    } else if (pb) {
+      pb[c - a.cols] = sum;
+    }
   }
 }
 
 // dweight / dbias = sum of the blocks' partial sums, in block order within
-// each of eight interleaved chains.
-__global__ void __launch_bounds__(256) ln_param_sum_kernel(const float* __restrict__ part, int blocks, int64_t cols,
+// each of eight interleaved chains.  V neighbouring columns per lane.
+template <int V>
+__global__ void __launch_bounds__(256) ln_param_sum_kernel(const float* __restrict__ part, int blocks, int cols,
                                                            float* dw, float* db) {
-  __shared__ float red[8][33];
+  griddep_wait();
+  __shared__ float red[8][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int c = (blockIdx.x * 32 + lane) * V;
   float* out = blockIdx.y ? db : dw;
   if (!out) return;
-  float s = 0.0f;
-  if (c < cols)
-    for (int b = warp; b < blocks; b += 8) s += part[(static_cast<int64_t>(b) * 2 + blockIdx.y) * cols + c];
-  red[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < cols) {
-    s = 0.0f;
+  float s[V];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += red[k][lane];
-    out[c] = s;
+  for (int v = 0; v < V; ++v) s[v] = 0.0f;
+  if (c < cols) {
+    const float* p = part + static_cast<int64_t>(blockIdx.y) * cols + c;
+#pragma unroll 8
+    for (int b = warp; b < blocks; b += 8) {
+      const float* q = p + static_cast<int64_t>(b) * 2 * cols;
+      if constexpr (V == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(q));
+        s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
+      } else {
+        s[0] += __ldcg(q);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) red[warp][lane * V + v] = s[v];
+  __syncthreads();
+  const int col = blockIdx.x * 32 * V + threadIdx.x;
+  if (threadIdx.x < 32 * V && col < cols) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += red[k][threadIdx.x];
+    out[col] = sum;
   }
 }
 
@@ -468,14 +646,14 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(const LnBwdArgs a) {
   const float mean = __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
   const uint64_t base = FUSED ? drop_base(a.drop) : 0;
   float s1 = 0.0f, s2 = 0.0f;
-  for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256) {
+  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
     const Raw8<T> dy = load_cols<false>(dyr, c0, a.cols, lane);
     const Raw8<T> z = load_cols<false>(zr, c0, a.cols, lane);
     Raw8<W> w;
     if (wr) w = load_cols<false>(wr, c0, a.cols, lane);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float h = col_in<false>(c0, lane, e, a.cols) ? (raw_f32(z, e) - mean) * rstd : 0.0f;
+      const float h = (raw_f32(z, e) - mean) * rstd;  // past the end dY = 0
       const float gr = wr ? raw_f32(dy, e) * raw_f32(w, e) : raw_f32(dy, e);
       s1 += gr;
       s2 = fmaf(gr, h, s2);
@@ -483,21 +661,22 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(const LnBwdArgs a) {
   }
   s1 = row_sum(s1, red[0], warp, 0, 32) * a.inv_n;
   s2 = row_sum(s2, red[1], warp, 0, 32) * a.inv_n;
-  for (int64_t c0 = static_cast<int64_t>(warp) * 256; c0 < a.cols; c0 += 32 * 256) {
+  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
     const Raw8<T> dy = load_cols<false>(dyr, c0, a.cols, lane);
     const Raw8<T> z = load_cols<false>(zr, c0, a.cols, lane);
     Raw8<W> w;
     if (wr) w = load_cols<false>(wr, c0, a.cols, lane);
     Raw8<T> dz;
     if (FUSED && a.dz) dz = load_cols<false>(static_cast<const T*>(a.dz) + at, c0, a.cols, lane);
-    float v[8];
+    F2 v[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float h = (raw_f32(z, e) - mean) * rstd;
-      v[e] = grad_value(raw_f32(dy, e), h, wr ? raw_f32(w, e) : 1.0f, s1, s2, rstd);
-      if (FUSED && a.dz) v[e] += raw_f32(dz, e);
+    for (int p = 0; p < 4; ++p) {
+      const F2 h = mul2(add2(raw_f2(z, p), f2_all(-mean)), f2_all(rstd));
+      const F2 g = fma2(raw_f2(dy, p), wr ? raw_f2(w, p) : f2_all(1.0f), f2_all(-s1));
+      v[p] = mul2(fma2(h, f2_all(-s2), g), f2_all(rstd));
+      if (FUSED && a.dz) v[p] = add2(v[p], raw_f2(dz, p));
     }
-    store_grad<T, false, FUSED>(a, row, c0, lane, base, v);
+    store_grad<T, false, FUSED>(a, row, at, c0, lane, base, v);
   }
 }
 
@@ -505,7 +684,7 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(const LnBwdArgs a) {
 // the rows y, y + gridDim.y, ...
 template <typename T>
 __global__ void __launch_bounds__(256) ln_param_long_kernel(const LnBwdArgs a) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= a.cols) return;
   float sw = 0.0f, sb = 0.0f;
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
@@ -529,15 +708,14 @@ int warps_for(int64_t cols, int groups) {
 
 template <typename T, typename W, bool VEC, bool FUSED>
 cudaError_t launch_fwd(LnFwdArgs a, cudaStream_t stream) {
-  if (a.cols > 32 * 256 * kFwdMaxGroups) {
+  if (a.cols > kFwdWarps * 256 * kFwdMaxGroups) {
     ln_fwd_long_kernel<T, W, FUSED><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
     return cudaGetLastError();
   }
   // Few rows: one step per warp where 32 warps allow it, for latency.
   // Otherwise four steps, so that several rows share an SM.
   int groups = kFwdMaxGroups;
-  if (a.rows <= 2 * device_sm_count())
-    for (groups = 1; groups < kFwdMaxGroups && warps_for(a.cols, groups) > 32;) groups *= 2;
+  if (a.rows <= 2 * device_sm_count() && a.cols <= 2 * kFwdWarps * 256) groups = 1;
   a.wpr = warps_for(a.cols, groups);
   while (groups > 1 && static_cast<int64_t>(a.wpr) * 256 * (groups / 2) >= a.cols) groups /= 2;
   const int warps = std::max(a.wpr, 4);
@@ -566,18 +744,13 @@ cudaError_t launch_ln_fwd(const LnFwdArgs& a, int32_t dtype, int32_t wdtype, boo
                          : launch_fwd_any<__half, float>(a, vec, fused, stream);
 }
 
-// Stages of the ring for these rows (0: a stage does not fit).
-int ring_stages(int64_t stage_bytes) {
-  return static_cast<int>(std::min<int64_t>(kMaxStages, kRingBytes / stage_bytes));
-}
-
-template <typename T, typename W, bool RING, bool FUSED>
+template <typename T, typename W, bool VEC, bool FUSED>
 cudaError_t launch_bwd_rows(const LnBwdArgs& a, int grid, size_t smem, cudaStream_t stream) {
-  auto kern = ln_bwd_kernel<T, W, RING, FUSED>;
+  auto kern = ln_bwd_kernel<T, W, VEC, FUSED>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes));
   if (e != cudaSuccess) return e;
-  kern<<<grid, kBwdWarps * 32, smem, stream>>>(a);
+  kern<<<grid, kBwdThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -585,7 +758,13 @@ template <typename T, typename W, bool FUSED>
 cudaError_t launch_bwd(LnBwdArgs a, bool vec, float* dw, float* db, cudaStream_t stream) {
   int blocks;
   cudaError_t e;
-  if (a.cols > kBwdCols) {
+  a.wpr = warps_for(std::min(a.cols, kBwdCols), kBwdGroups);
+  const int rpi = kBwdWarps / a.wpr;
+  // Room for a stage's rows at any alignment.
+  a.tensor_bytes = static_cast<uint32_t>((static_cast<int64_t>(rpi) * std::min(a.cols, kBwdCols) * sizeof(T) + 15 + 127) / 128 * 128);
+  const int64_t stage = static_cast<int64_t>(a.tensor_bytes) * (FUSED && a.dz ? 3 : 2);
+  a.stages = static_cast<int>(std::min<int64_t>(kMaxStages, kRingBytes / stage));
+  if (a.cols > kBwdCols || a.stages < 2) {
     ln_bwd_long_kernel<T, W, FUSED><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
     e = cudaGetLastError();
     blocks = static_cast<int>(std::min<int64_t>(a.rows, 64));
@@ -595,23 +774,30 @@ cudaError_t launch_bwd(LnBwdArgs a, bool vec, float* dw, float* db, cudaStream_t
       e = cudaGetLastError();
     }
   } else {
-    a.wpr = warps_for(a.cols, kBwdGroups);
-    const int rpi = kBwdWarps / a.wpr;
     const int64_t steps = (a.rows + rpi - 1) / rpi;
     blocks = static_cast<int>(std::min<int64_t>(steps, std::min(device_sm_count(), kBwdMaxBlocks)));
-    a.tensor_bytes = static_cast<uint32_t>(rpi * a.cols * sizeof(T));
-    const int64_t stage = static_cast<int64_t>(a.tensor_bytes) * (FUSED && a.dz ? 3 : 2);
-    a.stages = ring_stages(stage);
-    const size_t acc = rpi > 1 ? static_cast<size_t>(a.cols) * 8 : 0;  // sums of the row slots
-    if (vec && a.stages > 0)
-      e = launch_bwd_rows<T, W, true, FUSED>(a, blocks, std::max<size_t>(a.stages * stage, acc), stream);
-    else
-      e = launch_bwd_rows<T, W, false, FUSED>(a, blocks, std::max<size_t>(acc, 16), stream);
+    if (blocks == 1) {  // its sums are the result
+      a.part = nullptr;
+      a.dw = dw;
+      a.db = db;
+    }
+    const size_t acc = static_cast<size_t>(rpi) * a.cols * 8;  // sums of the row slots
+    const size_t smem = std::max<size_t>(a.stages * stage, acc);
+    e = vec ? launch_bwd_rows<T, W, true, FUSED>(a, blocks, smem, stream)
+            : launch_bwd_rows<T, W, false, FUSED>(a, blocks, smem, stream);
   }
   if (e != cudaSuccess || !a.part) return e;
-  ln_param_sum_kernel<<<dim3(static_cast<unsigned>((a.cols + 31) / 32), 2), 256, 0, stream>>>(a.part, blocks, a.cols,
-                                                                                             dw, db);
-  return cudaGetLastError();
+  const int v = a.cols % 4 == 0 ? 4 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.cols + 32 * v - 1) / (32 * v)), 2, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = pdl_attribute();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const float* part = a.part;
+  return v == 4 ? cudaLaunchKernelEx(&cfg, ln_param_sum_kernel<4>, part, blocks, a.cols, dw, db)
+                : cudaLaunchKernelEx(&cfg, ln_param_sum_kernel<1>, part, blocks, a.cols, dw, db);
 }
 
 template <typename T, typename W>
@@ -649,7 +835,7 @@ qlora_status fwd_call(LnFwdArgs& a, int64_t rows, int64_t cols, int32_t dtype, i
       !aligned_to(a.w, ws) || !aligned_to(a.b, ws) || !aligned_to(a.mean, 4) || !aligned_to(a.rstd, 4))
     return QLORA_ERR_ALIGNMENT;
   a.rows = rows;
-  a.cols = cols;
+  a.cols = static_cast<int>(cols);
   a.eps = eps;
   a.inv_n = static_cast<float>(1.0 / static_cast<double>(cols));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -672,7 +858,7 @@ qlora_status bwd_call(LnBwdArgs& a, int64_t rows, int64_t cols, int32_t dtype, i
   if (!workspace || ws_bytes < ln_workspace_bytes(cols)) return QLORA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
   a.rows = rows;
-  a.cols = cols;
+  a.cols = static_cast<int>(cols);
   a.inv_n = static_cast<float>(1.0 / static_cast<double>(cols));
   a.status = static_cast<int*>(workspace);
   a.wait_ns = wait_limit_ns();

@@ -15,6 +15,7 @@ struct Raw8 {
   uint32_t w[sizeof(T) * 2];
 };
 
+// Single elements.
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -75,6 +76,8 @@ __device__ __forceinline__ Raw8<float> raw_from<float>(const float (&v)[8]) {
   return r;
 }
 
+__device__ __forceinline__ bool aligned_group(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // Group transfers through 16-byte vectors (the address is 16-byte aligned).
 // "Stream" marks data that is touched once.
 template <typename T>
@@ -110,44 +113,123 @@ __device__ __forceinline__ void store_group_stream(T* p, const Raw8<T>& r) {
     __stcs(reinterpret_cast<uint4*>(p) + i, make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]));
 }
 
+// ---------------------------------------------------------------- pairs of float32
+// Two float32 values in a 64-bit register: one instruction adds, multiplies or
+// multiply-adds both.
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ F2 f2_all(float v) { return f2(v, v); }
+__device__ __forceinline__ float2 f2_get(F2 a) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ float f2_sum(F2 a) {
+  const float2 d = f2_get(a);
+  return d.x + d.y;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// Elements 2 p and 2 p + 1 of a group.
+template <typename T>
+__device__ __forceinline__ F2 raw_f2(const Raw8<T>& r, int p) { return f2(raw_f32(r, 2 * p), raw_f32(r, 2 * p + 1)); }
+
+// A group from four pairs, each value rounded once to T.
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw_from_pairs(const F2 (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const float2 d = f2_get(v[p]);
+    f[2 * p] = d.x;
+    f[2 * p + 1] = d.y;
+  }
+  return raw_from<T>(f);
+}
+
 // ---------------------------------------------------------------- columns of a warp
 // A warp owns 256 consecutive columns of a row at a time, eight per lane.
 // With aligned rows lane l holds columns 8 l .. 8 l + 7 (one group); with
 // ragged rows it holds l, l + 32, ... so that scalar accesses coalesce.
+// Column numbers stay below 2^31 (check_rows leaves room for the last step).
 template <bool VEC>
 __device__ __forceinline__ int warp_col(int lane, int e) { return VEC ? lane * 8 + e : lane + 32 * e; }
 
-// The warp's 8 values per lane of row[c0 ..], `fill` past the end.
-template <bool VEC, typename T>
-__device__ __forceinline__ Raw8<T> load_cols(const T* row, int64_t c0, int64_t cols, int lane) {
-  if constexpr (VEC) {
-    const int64_t c = c0 + lane * 8;
-    if (c < cols) return load_group(row + c);
-    Raw8<T> z;
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw_zero() {
+  Raw8<T> z;
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) * 2; ++i) z.w[i] = 0;
-    return z;
-  } else {
-    float v[8];
+  for (int i = 0; i < static_cast<int>(sizeof(T)) * 2; ++i) z.w[i] = 0;
+  return z;
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw_ones() {
+  const float v[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+  return raw_from<T>(v);
+}
+
+// The lane's eight columns of row[c0 ..] (global or shared memory), zeros past
+// the end.
+template <bool VEC, typename T>
+__device__ __forceinline__ Raw8<T> load_cols(const T* row, int c0, int cols, int lane) {
+  if constexpr (VEC) {
+    const int c = c0 + lane * 8;
+    return c < cols ? load_group(row + c) : raw_zero<T>();
+  } else if constexpr (sizeof(T) == 4) {
+    Raw8<T> r;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t c = c0 + lane + 32 * e;
-      v[e] = c < cols ? to_f32(row[c]) : 0.0f;
+      const int c = c0 + lane + 32 * e;
+      r.w[e] = c < cols ? reinterpret_cast<const uint32_t*>(row)[c] : 0u;
     }
-    return raw_from<T>(v);  // exact: the values came from T
+    return r;
+  } else {
+    Raw8<T> r;
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = c0 + lane + 32 * e;
+      h[e] = c < cols ? reinterpret_cast<const uint16_t*>(row)[c] : 0u;
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) r.w[p] = h[2 * p] | (h[2 * p + 1] << 16);
+    return r;
   }
 }
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store_cols(T* row, int64_t c0, int64_t cols, int lane, const float (&v)[8]) {
+__device__ __forceinline__ void store_cols(T* row, int c0, int cols, int lane, const Raw8<T>& r) {
   if constexpr (VEC) {
-    const int64_t c = c0 + lane * 8;
-    if (c < cols) store_group(row + c, raw_from<T>(v));
+    const int c = c0 + lane * 8;
+    if (c < cols) store_group(row + c, r);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int64_t c = c0 + lane + 32 * e;
-      if (c < cols) row[c] = from_f32<T>(v[e]);
+      const int c = c0 + lane + 32 * e;
+      if (c < cols) {
+        if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(row)[c] = r.w[e];
+        else reinterpret_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(r.w[e >> 1] >> (16 * (e & 1)));
+      }
     }
   }
 }
@@ -192,33 +274,40 @@ __device__ __forceinline__ uint64_t drop_base(const DropArgs& d) {
   return d.offset + (d.offset_dev ? *d.offset_dev : 0);
 }
 
-// Bit e is set when element e of the group with this counter is kept.
-__device__ __forceinline__ uint32_t keep_bits(const DropArgs& d, uint64_t counter) {
-  const Draws r = philox(counter, d.seed);
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t draw = (e & 1) ? (r.w[e >> 1] >> 16) : (r.w[e >> 1] & 0xFFFFu);
-    m |= (draw >= d.threshold ? 1u : 0u) << e;
+// Which of a lane's eight elements are kept.
+struct KeepGroup {  // of one group, straight from its draws
+  Draws r;
+  uint32_t threshold;
+  __device__ __forceinline__ bool operator()(int e) const {
+    return ((e & 1) ? (r.w[e >> 1] >> 16) : (r.w[e >> 1] & 0xFFFFu)) >= threshold;
   }
-  return m;
+};
+struct KeepBits {  // bit e: element e
+  uint32_t bits;
+  __device__ __forceinline__ bool operator()(int e) const { return (bits >> e) & 1u; }
+};
+
+__device__ __forceinline__ KeepGroup keep_group(const DropArgs& d, uint64_t counter) {
+  return KeepGroup{philox(counter, d.seed), d.threshold};
 }
 
 // The same for the eight columns a lane holds (warp_col) of the 256 at
 // `counter0` (the counter of the warp's first group).  All lanes take part.
 template <bool VEC>
-__device__ __forceinline__ uint32_t keep_bits_cols(const DropArgs& d, uint64_t counter0, int lane) {
-  const uint32_t own = keep_bits(d, counter0 + lane);
+__device__ __forceinline__ auto keep_cols(const DropArgs& d, uint64_t counter0, int lane) {
+  const KeepGroup own = keep_group(d, counter0 + lane);
   if constexpr (VEC) {
     return own;
   } else {
-    uint32_t m = 0;
+    uint32_t bits = 0, m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) bits |= (own(e) ? 1u : 0u) << e;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int col = lane + 32 * e;
-      m |= ((__shfl_sync(0xFFFFFFFFu, own, col >> 3) >> (col & 7)) & 1u) << e;
+      m |= ((__shfl_sync(0xFFFFFFFFu, bits, col >> 3) >> (col & 7)) & 1u) << e;
     }
-    return m;
+    return KeepBits{m};
   }
 }
 

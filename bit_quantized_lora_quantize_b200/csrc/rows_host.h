@@ -24,7 +24,7 @@ inline bool vector_rows(const void* p, int64_t cols) { return cols % 8 == 0 && a
 
 inline qlora_status check_rows(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0) return QLORA_ERR_INVALID_ARG;
-  if (rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31) || rows > kMaxRowElements / cols)
+  if (rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31) - 65536 || rows > kMaxRowElements / cols)
     return QLORA_ERR_UNSUPPORTED;
   return QLORA_OK;
 }

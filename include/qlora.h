@@ -289,8 +289,9 @@ QLORA_API qlora_status qlora_silu_gate_bwd(const uint16_t* G, const uint16_t* U,
  * [rows x cols], row-major and contiguous, of one element type `dtype`;
  * pointers need the alignment of their elements only (rows of whole 16-byte
  * vectors take wider accesses).  Arithmetic is float32 with one rounding per
- * output.  rows and cols are at least 1 and below 2^31, rows * cols at most
- * 2^40 (QLORA_ERR_UNSUPPORTED).  Outputs may not alias inputs.  Glue between
+ * output.  rows and cols are at least 1, rows below 2^31, cols below
+ * 2^31 - 2^16, rows * cols at most 2^40 (QLORA_ERR_UNSUPPORTED).  Outputs may
+ * not alias inputs.  Glue between
  * LoRA linears, like the SiLU gate: the pages have no counterpart.
  */
 typedef enum { QLORA_DTYPE_BF16 = 0, QLORA_DTYPE_FP16 = 1, QLORA_DTYPE_FP32 = 2 } qlora_dtype;
