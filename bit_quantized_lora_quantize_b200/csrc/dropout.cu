@@ -68,15 +68,15 @@ __global__ void __launch_bounds__(kDropThreads)
   const int64_t row = chunk / chunks_per_row;
   const int c0 = static_cast<int>(chunk - row * chunks_per_row) * 256;
   const int64_t at = row * cols;
-  const Raw8<T> x = load_cols<false>(X + at, c0, cols, lane);
+  const Raw8<T> x = load_cols<kRagged>(X + at, c0, cols, lane);
   Raw8<T> r;
-  if (RES) r = load_cols<false>(R + at, c0, cols, lane);
-  const KeepBits keep = keep_cols<false>(d, drop_base(d) + row * d.groups + c0 / 8, lane);
+  if (RES) r = load_cols<kRagged>(R + at, c0, cols, lane);
+  const KeepBits keep = keep_cols<kRagged>(d, drop_base(d) + row * d.groups + c0 / 8, lane);
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     v[e] = drop_value(raw_f32(x, e), RES ? raw_f32(r, e) : 0.0f, keep(e), d.gain);
-  store_cols<false>(Y + at, c0, cols, lane, raw_from<T>(v));
+  store_cols<kRagged>(Y + at, c0, cols, lane, raw_from<T>(v));
 }
 
 template <typename T, bool RES>

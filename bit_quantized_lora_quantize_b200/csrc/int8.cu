@@ -129,7 +129,7 @@ struct RowScale {
   }
 };
 
-template <bool VEC, typename T>
+template <int VEC, typename T>
 __device__ __forceinline__ void store_codes(const QuantArgs& a, int64_t row, int c0, int lane, const RowScale& rs,
                                             const Raw8<T>& x) {
   const int padded = (a.cols + 15) / 16 * 16;  // columns past the end hold 0
@@ -138,7 +138,7 @@ __device__ __forceinline__ void store_codes(const QuantArgs& a, int64_t row, int
   rs.codes(x, k);
   if constexpr (VEC) {
     const int c = c0 + lane * 8;
-    if (c < padded)
+    if (VEC == kWhole || c < padded)
       *reinterpret_cast<uint2*>(out + c) =
           make_uint2(prmt(prmt(k[0], k[1], 0x0040), prmt(k[2], k[3], 0x0040), 0x5410),
                      prmt(prmt(k[4], k[5], 0x0040), prmt(k[6], k[7], 0x0040), 0x5410));
@@ -154,20 +154,19 @@ __device__ __forceinline__ void store_codes(const QuantArgs& a, int64_t row, int
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf, int warp, int first, int wpr) {
   v = __reduce_max_sync(kAll, v);
   if (wpr == 1) return v;
-  if ((threadIdx.x & 31) == 0) buf[warp] = v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) buf[warp] = v;
   __syncthreads();
-  uint32_t m = 0;
-  for (int i = 0; i < wpr; ++i) m = max(m, buf[first + i]);
-  return m;
+  return __reduce_max_sync(kAll, buf[first + (lane & (wpr - 1))]);
 }
 
-template <typename T, int G, bool VEC>
+template <typename T, int G, int VEC>
 __global__ void __launch_bounds__(1024) quantize_rows_kernel(const QuantArgs a) {
   griddep_launch_dependents();  // a product that follows may load its weight meanwhile
   __shared__ uint32_t red[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = warp % a.wpr, first = warp - part;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32 / a.wpr) + warp / a.wpr;
+  const int part = warp & (a.wpr - 1), first = warp - part, shift = __ffs(a.wpr) - 1;  // wpr is a power of two
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> (5 + shift)) + (warp >> shift);
   const bool valid = row < a.rows;
   const T* xr = static_cast<const T*>(a.x) + row * a.cols;
   Raw8<T> x[G];
@@ -203,11 +202,11 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const QuantArg
   const T* xr = static_cast<const T*>(a.x) + row * a.cols;
   uint32_t m = 0;
   for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256)
-    m = max(m, abs_max(load_cols<false>(xr, c0, a.cols, lane)));
+    m = max(m, abs_max(load_cols<kRagged>(xr, c0, a.cols, lane)));
   const RowScale rs(row_max(m, red, warp, 0, 32));
   if (threadIdx.x == 0) a.scale[row] = rs.scale;
   for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256)
-    store_codes<false>(a, row, c0, lane, rs, load_cols<false>(xr, c0, a.cols, lane));
+    store_codes<kRagged>(a, row, c0, lane, rs, load_cols<kRagged>(xr, c0, a.cols, lane));
 }
 
 template <typename T>
@@ -223,12 +222,15 @@ cudaError_t launch_quantize_rows(QuantArgs a, cudaStream_t stream) {
   while (static_cast<int64_t>(a.wpr) * 256 * groups < a.cols) a.wpr *= 2;
   const int warps = std::max(a.wpr, 4);
   const unsigned grid = static_cast<unsigned>((a.rows + warps / a.wpr - 1) / (warps / a.wpr));
+  const int layout = vec ? aligned_layout(a.cols) : kRagged;
   if (groups == 1) {
-    if (vec) quantize_rows_kernel<T, 1, true><<<grid, warps * 32, 0, stream>>>(a);
-    else quantize_rows_kernel<T, 1, false><<<grid, warps * 32, 0, stream>>>(a);
+    if (layout == kWhole) quantize_rows_kernel<T, 1, kWhole><<<grid, warps * 32, 0, stream>>>(a);
+    else if (layout == kAligned) quantize_rows_kernel<T, 1, kAligned><<<grid, warps * 32, 0, stream>>>(a);
+    else quantize_rows_kernel<T, 1, kRagged><<<grid, warps * 32, 0, stream>>>(a);
   } else {
-    if (vec) quantize_rows_kernel<T, kQuantGroups, true><<<grid, warps * 32, 0, stream>>>(a);
-    else quantize_rows_kernel<T, kQuantGroups, false><<<grid, warps * 32, 0, stream>>>(a);
+    if (layout == kWhole) quantize_rows_kernel<T, kQuantGroups, kWhole><<<grid, warps * 32, 0, stream>>>(a);
+    else if (layout == kAligned) quantize_rows_kernel<T, kQuantGroups, kAligned><<<grid, warps * 32, 0, stream>>>(a);
+    else quantize_rows_kernel<T, kQuantGroups, kRagged><<<grid, warps * 32, 0, stream>>>(a);
   }
   return cudaGetLastError();
 }

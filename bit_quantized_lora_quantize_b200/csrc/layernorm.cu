@@ -59,19 +59,22 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the wpr warps of a row; `buf` holds one float per warp.  Every
-// thread of the block calls it.
+// Sum over the wpr warps of a row (a power of two); `buf` holds one float per
+// warp.  Every thread of the block calls it.
 __device__ __forceinline__ float row_sum(float v, float* buf, int warp, int first, int wpr) {
   v = warp_sum(v);
   if (wpr == 1) return v;
-  if ((threadIdx.x & 31) == 0) buf[warp] = v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) buf[warp] = v;
   __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < wpr; ++i) s += buf[first + i];
-  return s;
+  v = buf[first + (lane & (wpr - 1))];
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2)
+    if (o < wpr) v += __shfl_xor_sync(kAll, v, o);
+  return v;
 }
 
-template <bool VEC>
+template <int VEC>
 __device__ __forceinline__ bool col_in(int c0, int lane, int e, int cols) {
   return c0 + warp_col<VEC>(lane, e) < cols;
 }
@@ -94,7 +97,7 @@ struct LnFwdArgs {
 
 // Values of one lane's eight columns after the residual dropout, rounded to
 // T and stored to Z.
-template <typename T, bool VEC>
+template <typename T, int VEC>
 __device__ __forceinline__ Raw8<T> add_dropped(const LnFwdArgs& a, int64_t row, int c0, int lane, uint64_t base,
                                                const Raw8<T>& x, const Raw8<T>& r) {
   const auto keep = keep_cols<VEC>(a.drop, base + row * a.drop.groups + c0 / 8, lane);
@@ -108,52 +111,52 @@ __device__ __forceinline__ Raw8<T> add_dropped(const LnFwdArgs& a, int64_t row, 
 
 // Sum of a lane's eight values (zeros past the end), and of their squared
 // distances from the mean.
-template <typename T>
-__device__ __forceinline__ float group_sum(const Raw8<T>& x) {
-  return f2_sum(add2(add2(raw_f2(x, 0), raw_f2(x, 1)), add2(raw_f2(x, 2), raw_f2(x, 3))));
+__device__ __forceinline__ float group_sum(const F2 (&x)[4]) {
+  return f2_sum(add2(add2(x[0], x[1]), add2(x[2], x[3])));
 }
-template <bool VEC, typename T>
-__device__ __forceinline__ float group_spread(const Raw8<T>& x, float mean, int c0, int lane, int cols) {
+template <int VEC>
+__device__ __forceinline__ float group_spread(const F2 (&x)[4], float mean, int c0, int lane, int cols) {
   const F2 m = f2_all(-mean);
   F2 q = 0;
-  if (c0 + 256 <= cols) {
+  if (VEC == kWhole || c0 + 256 <= cols) {
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const F2 d = add2(raw_f2(x, p), m);
+      const F2 d = add2(x[p], m);
       q = fma2(d, d, q);
     }
     return f2_sum(q);
   }
   float s = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float d = raw_f32(x, e) - mean;
-    if (col_in<VEC>(c0, lane, e, cols)) s = fmaf(d, d, s);
+  for (int p = 0; p < 4; ++p) {
+    const float2 d = f2_get(add2(x[p], m));
+    if (col_in<VEC>(c0, lane, 2 * p, cols)) s = fmaf(d.x, d.x, s);
+    if (col_in<VEC>(c0, lane, 2 * p + 1, cols)) s = fmaf(d.y, d.y, s);
   }
   return s;
 }
 
-template <typename T, typename W, bool VEC>
+template <typename T, typename W, int VEC>
 __device__ __forceinline__ void normalise(const LnFwdArgs& a, int64_t row, int c0, int lane, float mean, float rstd,
-                                          const Raw8<T>& x) {
+                                          const F2 (&x)[4]) {
   const Raw8<W> w = a.w ? load_cols<VEC>(static_cast<const W*>(a.w), c0, a.cols, lane) : raw_ones<W>();
   const Raw8<W> b = a.b ? load_cols<VEC>(static_cast<const W*>(a.b), c0, a.cols, lane) : raw_zero<W>();
   const F2 m = f2_all(-mean), r = f2_all(rstd);
   F2 v[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    const F2 h = mul2(add2(raw_f2(x, p), m), r);
+    const F2 h = mul2(add2(x[p], m), r);
     v[p] = fma2(h, raw_f2(w, p), raw_f2(b, p));
   }
   store_cols<VEC>(static_cast<T*>(a.y) + row * a.cols, c0, a.cols, lane, raw_from_pairs<T>(v));
 }
 
-template <typename T, typename W, int G, bool VEC, bool FUSED>
+template <typename T, typename W, int G, int VEC, bool FUSED>
 __global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kernel(const LnFwdArgs a) {
   __shared__ float red[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = warp % a.wpr, first = warp - part;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32 / a.wpr) + warp / a.wpr;
+  const int part = warp & (a.wpr - 1), first = warp - part, shift = __ffs(a.wpr) - 1;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> (5 + shift)) + (warp >> shift);
   const bool valid = row < a.rows;
   const T* xr = static_cast<const T*>(a.x) + row * a.cols;
   const T* rr = static_cast<const T*>(a.residual) + row * a.cols;
@@ -168,12 +171,14 @@ __global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kern
     }
   }
   const uint64_t base = FUSED ? drop_base(a.drop) : 0;
+  F2 v[G][4];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int c0 = (part + g * a.wpr) * 256;
     if (valid && c0 < a.cols) {
       if constexpr (FUSED) x[g] = add_dropped<T, VEC>(a, row, c0, lane, base, x[g], r[g]);
-      s += group_sum(x[g]);
+      raw_pairs(x[g], v[g]);
+      s += group_sum(v[g]);
     }
   }
   const float mean = row_sum(s, red[0], warp, first, a.wpr) * a.inv_n;
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kern
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int c0 = (part + g * a.wpr) * 256;
-    if (valid && c0 < a.cols) q += group_spread<VEC>(x[g], mean, c0, lane, a.cols);
+    if (valid && c0 < a.cols) q += group_spread<VEC>(v[g], mean, c0, lane, a.cols);
   }
   const float rstd = 1.0f / sqrtf(row_sum(q, red[1], warp, first, a.wpr) * a.inv_n + a.eps);
   if (!valid) return;
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kern
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int c0 = (part + g * a.wpr) * 256;
-    if (c0 < a.cols) normalise<T, W, VEC>(a, row, c0, lane, mean, rstd, x[g]);
+    if (c0 < a.cols) normalise<T, W, VEC>(a, row, c0, lane, mean, rstd, v[g]);
   }
 }
 
@@ -207,25 +212,33 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(const LnFwdArgs a) {
   const uint64_t base = FUSED ? drop_base(a.drop) : 0;
   float s = 0.0f;
   for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
-    Raw8<T> x = load_cols<false>(xr, c0, a.cols, lane);
+    Raw8<T> x = load_cols<kRagged>(xr, c0, a.cols, lane);
     if constexpr (FUSED)
-      x = add_dropped<T, false>(a, row, c0, lane, base, x,
-                                load_cols<false>(static_cast<const T*>(a.residual) + row * a.cols, c0, a.cols, lane));
-    s += group_sum(x);
+      x = add_dropped<T, kRagged>(a, row, c0, lane, base, x,
+                                load_cols<kRagged>(static_cast<const T*>(a.residual) + row * a.cols, c0, a.cols, lane));
+    F2 v[4];
+    raw_pairs(x, v);
+    s += group_sum(v);
   }
   const float mean = row_sum(s, red[0], warp, 0, 32) * a.inv_n;
   // Each thread reads back only what it stored itself.
   const T* zr = FUSED ? static_cast<const T*>(a.z) + row * a.cols : xr;
   float q = 0.0f;
-  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256)
-    q += group_spread<false>(load_cols<false>(zr, c0, a.cols, lane), mean, c0, lane, a.cols);
+  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
+    F2 v[4];
+    raw_pairs(load_cols<kRagged>(zr, c0, a.cols, lane), v);
+    q += group_spread<kRagged>(v, mean, c0, lane, a.cols);
+  }
   const float rstd = 1.0f / sqrtf(row_sum(q, red[1], warp, 0, 32) * a.inv_n + a.eps);
   if (threadIdx.x == 0) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
   }
-  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256)
-    normalise<T, W, false>(a, row, c0, lane, mean, rstd, load_cols<false>(zr, c0, a.cols, lane));
+  for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
+    F2 v[4];
+    raw_pairs(load_cols<kRagged>(zr, c0, a.cols, lane), v);
+    normalise<T, W, kRagged>(a, row, c0, lane, mean, rstd, v);
+  }
 }
 
 // ---------------------------------------------------------------- backward
@@ -261,7 +274,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // dz = rstd (dy w - s1 - h s2) [+ the gradient past the norm], four pairs of it
 // to memory, and dropout(dz) in the fused form.
-template <typename T, bool VEC, bool FUSED>
+template <typename T, int VEC, bool FUSED>
 __device__ __forceinline__ void store_grad(const LnBwdArgs& a, int64_t row, int64_t at, int c0, int lane, uint64_t base,
                                            const F2 (&v)[4]) {
   if constexpr (!FUSED) {
@@ -282,11 +295,12 @@ __device__ __forceinline__ void store_grad(const LnBwdArgs& a, int64_t row, int6
 
 // A lane's eight float32 values to row[c0 ..]; `row` is aligned for vectors when
 // VEC and the columns a multiple of eight.
-template <bool VEC>
+template <int VEC>
 __device__ __forceinline__ void store_pairs(float* row, int c0, int cols, int lane, const F2 (&v)[4]) {
+  if (c0 >= cols) return;
   if (VEC && aligned_group(row)) {
     const int c = c0 + lane * 8;
-    if (c < cols) store_group(row + c, raw_from_pairs<float>(v));
+    if (VEC == kWhole || c < cols) store_group(row + c, raw_from_pairs<float>(v));
     return;
   }
 #pragma unroll
@@ -361,7 +375,7 @@ __device__ __forceinline__ float2 row_pair(const float (*red)[2], int first, int
 // one barrier per step, with independent work on both sides of it.  A warp of
 // its own feeds the ring: its address arithmetic would otherwise hold up the
 // barrier of every step (2 us a step before, whatever the columns).
-template <typename T, typename W, bool VEC, bool FUSED>
+template <typename T, typename W, int VEC, bool FUSED>
 __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs a) {
   constexpr int G = kBwdGroups;
   extern __shared__ __align__(128) uint8_t ring[];
@@ -371,8 +385,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = warp % a.wpr, first = warp - part, slot = warp / a.wpr;
-  const int rpi = kBwdWarps / a.wpr;  // rows per step of the block
+  const int log = __ffs(a.wpr) - 1, part = warp & (a.wpr - 1), first = warp - part, slot = warp >> log;
+  const int rpi = kBwdWarps >> log;  // rows per step of the block
   const int64_t steps = (a.rows + rpi - 1) / rpi;
   const int mine = static_cast<int>((steps - blockIdx.x + gridDim.x - 1) / gridDim.x);
   const bool has_dz = FUSED && a.dz;
@@ -443,7 +457,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int c0 = (part + g * a.wpr) * 256;
-    const Raw8<W> raw = a.w ? load_cols<VEC>(static_cast<const W*>(a.w), c0, a.cols, lane) : raw_ones<W>();
+    const Raw8<W> raw =
+        a.w && c0 < a.cols ? load_cols<VEC>(static_cast<const W*>(a.w), c0, a.cols, lane) : raw_ones<W>();
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       w[g][p] = raw_f2(raw, p);
@@ -455,13 +470,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
   const int64_t stride = static_cast<int64_t>(gridDim.x) * rpi, stride_at = stride * a.cols;
   struct Row {
     int64_t row, at;  // row number, first element
-    const uint8_t* stage;
+    uint32_t stage;  // its place in the ring
     float mean, rstd;
   };
   // The row's columns of tensor t in the ring (a stage starts at its first row).
+  const uint32_t slot_bytes = static_cast<uint32_t>(slot * a.cols * sizeof(T));
   const auto row_in = [&](const Row& r, int t) {
     const uint32_t shift = VEC ? 0u : ring_of[t].shift(r.at - static_cast<int64_t>(slot) * a.cols);
-    return reinterpret_cast<const T*>(r.stage + t * a.tensor_bytes + shift) + slot * a.cols;
+    return r.stage + t * a.tensor_bytes + shift + slot_bytes;
+  };
+  // 32-bit offsets from the array's name, so that the accesses stay shared-memory ones.
+  const auto load_in = [&](uint32_t row, int c0) {
+    return load_cols<VEC>(reinterpret_cast<const T*>(ring + row), c0, a.cols, lane);
   };
   const auto sums = [&](Row& r, int s, float(*out)[2]) {
     F2 s1 = 0, s2 = 0;
@@ -469,15 +489,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
     r.mean = st.x;
     r.rstd = st.y;
     if (r.row < a.rows) {
-      const T* dyr = row_in(r, 0);
-      const T* zr = row_in(r, 1);
+      const uint32_t dyr = row_in(r, 0), zr = row_in(r, 1);
       const F2 nm = f2_all(-r.mean), rs = f2_all(r.rstd);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const int c0 = (part + g * a.wpr) * 256;
         if (c0 < a.cols) {
           // columns past the end hold dY = 0 and add nothing
-          const Raw8<T> dy = load_cols<VEC>(dyr, c0, a.cols, lane), z = load_cols<VEC>(zr, c0, a.cols, lane);
+          const Raw8<T> dy = load_in(dyr, c0);
+          const Raw8<T> z = load_in(zr, c0);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             const F2 d = raw_f2(dy, p), h = mul2(add2(raw_f2(z, p), nm), rs), gr = mul2(d, w[g][p]);
@@ -502,7 +522,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
   Row cur, next;
   next.row = static_cast<int64_t>(blockIdx.x) * rpi + slot;
   next.at = next.row * a.cols;
-  next.stage = ring;
+  next.stage = 0;
   int s = 0;             // stage of `next`
   uint32_t parity = 0;
   const auto advance = [&] {
@@ -512,7 +532,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
       s = 0;
       parity ^= 1;
     }
-    next.stage = ring + s * stage_bytes;
+    next.stage = s * stage_bytes;
   };
   // The computing warps' own barrier.
   const auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kBwdWarps * 32) : "memory"); };
@@ -523,30 +543,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
   sync();
   int s_cur = 0;
   for (int i = 0; i < mine; ++i) {
+    const float2 sum = row_pair(red[i & 1], first, a.wpr);
     if (i + 1 < mine) {
       mbar_wait(&full[s], parity, ctx);
       sums(next, s, red[(i + 1) & 1]);
     }
     if (cur.row < a.rows) {
-      const float2 sum = row_pair(red[i & 1], first, a.wpr);
+      // rstd (dy w - s1 - h s2) = rstd dy w - rstd s1 - (z - mean) rstd^2 s2
       const F2 nm = f2_all(-cur.mean), rs = f2_all(cur.rstd);
-      const F2 s1 = f2_all(-sum.x * a.inv_n), s2 = f2_all(-sum.y * a.inv_n);
-      const T* dyr = row_in(cur, 0);
-      const T* zr = row_in(cur, 1);
-      const T* dzr = row_in(cur, 2);
+      const F2 k1 = f2_all(-cur.rstd * (sum.x * a.inv_n));
+      const F2 k2 = f2_all(-cur.rstd * (cur.rstd * (sum.y * a.inv_n)));
+      const uint32_t dyr = row_in(cur, 0), zr = row_in(cur, 1), dzr = row_in(cur, 2);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const int c0 = (part + g * a.wpr) * 256;
         if (c0 < a.cols) {
-          const Raw8<T> dy = load_cols<VEC>(dyr, c0, a.cols, lane), z = load_cols<VEC>(zr, c0, a.cols, lane);
+          const Raw8<T> dy = load_in(dyr, c0);
+          const Raw8<T> z = load_in(zr, c0);
           F2 v[4];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const F2 h = mul2(add2(raw_f2(z, p), nm), rs);
-            v[p] = mul2(fma2(h, s2, fma2(raw_f2(dy, p), w[g][p], s1)), rs);
-          }
+          for (int p = 0; p < 4; ++p)
+            v[p] = fma2(mul2(raw_f2(dy, p), w[g][p]), rs, fma2(add2(raw_f2(z, p), nm), k2, k1));
           if (has_dz) {
-            const Raw8<T> dz = load_cols<VEC>(dzr, c0, a.cols, lane);
+            const Raw8<T> dz = load_in(dzr, c0);
 #pragma unroll
             for (int p = 0; p < 4; ++p) v[p] = add2(v[p], raw_f2(dz, p));
           }
@@ -595,40 +614,48 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
 }
 
 // dweight / dbias = sum of the blocks' partial sums, in block order within
-// each of eight interleaved chains.  V neighbouring columns per lane.
+// each of 16 interleaved chains.  V neighbouring columns per lane; all of a
+// warp's loads are in flight together.
+constexpr int kSumWarps = 16;
 template <int V>
-__global__ void __launch_bounds__(256) ln_param_sum_kernel(const float* __restrict__ part, int blocks, int cols,
-                                                           float* dw, float* db) {
-  griddep_wait();
-  __shared__ float red[8][32 * V];
+__global__ void __launch_bounds__(kSumWarps * 32) ln_param_sum_kernel(const float* __restrict__ part, int blocks,
+                                                                      int cols, float* dw, float* db) {
+  constexpr int kLoads = (kBwdMaxBlocks + kSumWarps - 1) / kSumWarps;
+  __shared__ float red[kSumWarps][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + lane) * V;
   float* out = blockIdx.y ? db : dw;
+  griddep_wait();
   if (!out) return;
-  float s[V];
+  float x[kLoads][V];
+  const float* p = part + (static_cast<int64_t>(warp) * 2 + blockIdx.y) * cols + c;
 #pragma unroll
-  for (int v = 0; v < V; ++v) s[v] = 0.0f;
-  if (c < cols) {
-    const float* p = part + static_cast<int64_t>(blockIdx.y) * cols + c;
-#pragma unroll 8
-    for (int b = warp; b < blocks; b += 8) {
-      const float* q = p + static_cast<int64_t>(b) * 2 * cols;
+  for (int k = 0; k < kLoads; ++k) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[k][v] = 0.0f;
+    if (c < cols && warp + k * kSumWarps < blocks) {
+      const float* q = p + static_cast<int64_t>(k) * kSumWarps * 2 * cols;
       if constexpr (V == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(q));
-        s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(q));
+        x[k][0] = f.x; x[k][1] = f.y; x[k][2] = f.z; x[k][3] = f.w;
       } else {
-        s[0] += __ldcg(q);
+        x[k][0] = __ldcg(q);
       }
     }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) red[warp][lane * V + v] = s[v];
+  for (int v = 0; v < V; ++v) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) s += x[k][v];
+    red[warp][lane * V + v] = s;
+  }
   __syncthreads();
   const int col = blockIdx.x * 32 * V + threadIdx.x;
   if (threadIdx.x < 32 * V && col < cols) {
     float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += red[k][threadIdx.x];
+    for (int k = 0; k < kSumWarps; ++k) sum += red[k][threadIdx.x];
     out[col] = sum;
   }
 }
@@ -647,10 +674,10 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(const LnBwdArgs a) {
   const uint64_t base = FUSED ? drop_base(a.drop) : 0;
   float s1 = 0.0f, s2 = 0.0f;
   for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
-    const Raw8<T> dy = load_cols<false>(dyr, c0, a.cols, lane);
-    const Raw8<T> z = load_cols<false>(zr, c0, a.cols, lane);
+    const Raw8<T> dy = load_cols<kRagged>(dyr, c0, a.cols, lane);
+    const Raw8<T> z = load_cols<kRagged>(zr, c0, a.cols, lane);
     Raw8<W> w;
-    if (wr) w = load_cols<false>(wr, c0, a.cols, lane);
+    if (wr) w = load_cols<kRagged>(wr, c0, a.cols, lane);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float h = (raw_f32(z, e) - mean) * rstd;  // past the end dY = 0
@@ -662,12 +689,12 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(const LnBwdArgs a) {
   s1 = row_sum(s1, red[0], warp, 0, 32) * a.inv_n;
   s2 = row_sum(s2, red[1], warp, 0, 32) * a.inv_n;
   for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
-    const Raw8<T> dy = load_cols<false>(dyr, c0, a.cols, lane);
-    const Raw8<T> z = load_cols<false>(zr, c0, a.cols, lane);
+    const Raw8<T> dy = load_cols<kRagged>(dyr, c0, a.cols, lane);
+    const Raw8<T> z = load_cols<kRagged>(zr, c0, a.cols, lane);
     Raw8<W> w;
-    if (wr) w = load_cols<false>(wr, c0, a.cols, lane);
+    if (wr) w = load_cols<kRagged>(wr, c0, a.cols, lane);
     Raw8<T> dz;
-    if (FUSED && a.dz) dz = load_cols<false>(static_cast<const T*>(a.dz) + at, c0, a.cols, lane);
+    if (FUSED && a.dz) dz = load_cols<kRagged>(static_cast<const T*>(a.dz) + at, c0, a.cols, lane);
     F2 v[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -676,7 +703,7 @@ __global__ void __launch_bounds__(1024) ln_bwd_long_kernel(const LnBwdArgs a) {
       v[p] = mul2(fma2(h, f2_all(-s2), g), f2_all(rstd));
       if (FUSED && a.dz) v[p] = add2(v[p], raw_f2(dz, p));
     }
-    store_grad<T, false, FUSED>(a, row, at, c0, lane, base, v);
+    store_grad<T, kRagged, FUSED>(a, row, at, c0, lane, base, v);
   }
 }
 
@@ -706,7 +733,7 @@ int warps_for(int64_t cols, int groups) {
   return w;
 }
 
-template <typename T, typename W, bool VEC, bool FUSED>
+template <typename T, typename W, int VEC, bool FUSED>
 cudaError_t launch_fwd(LnFwdArgs a, cudaStream_t stream) {
   if (a.cols > kFwdWarps * 256 * kFwdMaxGroups) {
     ln_fwd_long_kernel<T, W, FUSED><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
@@ -727,10 +754,16 @@ cudaError_t launch_fwd(LnFwdArgs a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <typename T, typename W, bool FUSED>
+cudaError_t launch_fwd_layout(const LnFwdArgs& a, bool vec, cudaStream_t stream) {
+  if (!vec) return launch_fwd<T, W, kRagged, FUSED>(a, stream);
+  return aligned_layout(a.cols) == kWhole ? launch_fwd<T, W, kWhole, FUSED>(a, stream)
+                                          : launch_fwd<T, W, kAligned, FUSED>(a, stream);
+}
+
 template <typename T, typename W>
 cudaError_t launch_fwd_any(const LnFwdArgs& a, bool vec, bool fused, cudaStream_t stream) {
-  if (fused) return vec ? launch_fwd<T, W, true, true>(a, stream) : launch_fwd<T, W, false, true>(a, stream);
-  return vec ? launch_fwd<T, W, true, false>(a, stream) : launch_fwd<T, W, false, false>(a, stream);
+  return fused ? launch_fwd_layout<T, W, true>(a, vec, stream) : launch_fwd_layout<T, W, false>(a, vec, stream);
 }
 
 cudaError_t launch_ln_fwd(const LnFwdArgs& a, int32_t dtype, int32_t wdtype, bool fused, cudaStream_t stream) {
@@ -744,7 +777,7 @@ cudaError_t launch_ln_fwd(const LnFwdArgs& a, int32_t dtype, int32_t wdtype, boo
                          : launch_fwd_any<__half, float>(a, vec, fused, stream);
 }
 
-template <typename T, typename W, bool VEC, bool FUSED>
+template <typename T, typename W, int VEC, bool FUSED>
 cudaError_t launch_bwd_rows(const LnBwdArgs& a, int grid, size_t smem, cudaStream_t stream) {
   auto kern = ln_bwd_kernel<T, W, VEC, FUSED>;
   const cudaError_t e =
@@ -783,14 +816,15 @@ cudaError_t launch_bwd(LnBwdArgs a, bool vec, float* dw, float* db, cudaStream_t
     }
     const size_t acc = static_cast<size_t>(rpi) * a.cols * 8;  // sums of the row slots
     const size_t smem = std::max<size_t>(a.stages * stage, acc);
-    e = vec ? launch_bwd_rows<T, W, true, FUSED>(a, blocks, smem, stream)
-            : launch_bwd_rows<T, W, false, FUSED>(a, blocks, smem, stream);
+    if (!vec) e = launch_bwd_rows<T, W, kRagged, FUSED>(a, blocks, smem, stream);
+    else if (aligned_layout(a.cols) == kWhole) e = launch_bwd_rows<T, W, kWhole, FUSED>(a, blocks, smem, stream);
+    else e = launch_bwd_rows<T, W, kAligned, FUSED>(a, blocks, smem, stream);
   }
   if (e != cudaSuccess || !a.part) return e;
   const int v = a.cols % 4 == 0 ? 4 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.cols + 32 * v - 1) / (32 * v)), 2, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(kSumWarps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr = pdl_attribute();
   cfg.attrs = &attr;

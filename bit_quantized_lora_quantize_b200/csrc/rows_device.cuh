@@ -54,7 +54,7 @@ __device__ __forceinline__ Raw8<__nv_bfloat16> raw_from<__nv_bfloat16>(const flo
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-    r.w[e] = __bfloat16_as_ushort(p.x) | (static_cast<uint32_t>(__bfloat16_as_ushort(p.y)) << 16);
+    r.w[e] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return r;
 }
@@ -64,7 +64,7 @@ __device__ __forceinline__ Raw8<__half> raw_from<__half>(const float (&v)[8]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const __half2 p = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-    r.w[e] = __half_as_ushort(p.x) | (static_cast<uint32_t>(__half_as_ushort(p.y)) << 16);
+    r.w[e] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return r;
 }
@@ -153,6 +153,13 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 template <typename T>
 __device__ __forceinline__ F2 raw_f2(const Raw8<T>& r, int p) { return f2(raw_f32(r, 2 * p), raw_f32(r, 2 * p + 1)); }
 
+// All four pairs.
+template <typename T>
+__device__ __forceinline__ void raw_pairs(const Raw8<T>& r, F2 (&v)[4]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) v[p] = raw_f2(r, p);
+}
+
 // A group from four pairs, each value rounded once to T.
 template <typename T>
 __device__ __forceinline__ Raw8<T> raw_from_pairs(const F2 (&v)[4]) {
@@ -169,9 +176,15 @@ __device__ __forceinline__ Raw8<T> raw_from_pairs(const F2 (&v)[4]) {
 // ---------------------------------------------------------------- columns of a warp
 // A warp owns 256 consecutive columns of a row at a time, eight per lane.
 // With aligned rows lane l holds columns 8 l .. 8 l + 7 (one group); with
-// ragged rows it holds l, l + 32, ... so that scalar accesses coalesce.
+// ragged rows it holds l, l + 32, ... so that scalar accesses coalesce.  The
+// template argument tells how rows lie:
+enum RowLayout {
+  kRagged = 0,   // anything
+  kAligned = 1,  // whole groups on 16-byte boundaries
+  kWhole = 2,    // the same, and a multiple of 256 columns: no lane is past the end
+};
 // Column numbers stay below 2^31 (check_rows leaves room for the last step).
-template <bool VEC>
+template <int VEC>
 __device__ __forceinline__ int warp_col(int lane, int e) { return VEC ? lane * 8 + e : lane + 32 * e; }
 
 template <typename T>
@@ -190,11 +203,11 @@ __device__ __forceinline__ Raw8<T> raw_ones() {
 
 // The lane's eight columns of row[c0 ..] (global or shared memory), zeros past
 // the end.
-template <bool VEC, typename T>
+template <int VEC, typename T>
 __device__ __forceinline__ Raw8<T> load_cols(const T* row, int c0, int cols, int lane) {
   if constexpr (VEC) {
     const int c = c0 + lane * 8;
-    return c < cols ? load_group(row + c) : raw_zero<T>();
+    return VEC == kWhole || c < cols ? load_group(row + c) : raw_zero<T>();
   } else if constexpr (sizeof(T) == 4) {
     Raw8<T> r;
 #pragma unroll
@@ -217,11 +230,11 @@ __device__ __forceinline__ Raw8<T> load_cols(const T* row, int c0, int cols, int
   }
 }
 
-template <bool VEC, typename T>
+template <int VEC, typename T>
 __device__ __forceinline__ void store_cols(T* row, int c0, int cols, int lane, const Raw8<T>& r) {
   if constexpr (VEC) {
     const int c = c0 + lane * 8;
-    if (c < cols) store_group(row + c, r);
+    if (VEC == kWhole || c < cols) store_group(row + c, r);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -293,7 +306,7 @@ __device__ __forceinline__ KeepGroup keep_group(const DropArgs& d, uint64_t coun
 
 // The same for the eight columns a lane holds (warp_col) of the 256 at
 // `counter0` (the counter of the warp's first group).  All lanes take part.
-template <bool VEC>
+template <int VEC>
 __device__ __forceinline__ auto keep_cols(const DropArgs& d, uint64_t counter0, int lane) {
   const KeepGroup own = keep_group(d, counter0 + lane);
   if constexpr (VEC) {

@@ -19,6 +19,8 @@ inline bool known_dtype(int32_t dtype) {
   return dtype == QLORA_DTYPE_BF16 || dtype == QLORA_DTYPE_FP16 || dtype == QLORA_DTYPE_FP32;
 }
 inline bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+// Layout that aligned rows of this many columns have.
+inline int aligned_layout(int64_t cols) { return cols % 256 == 0 ? kWhole : kAligned; }
 // Rows of whole 16-byte vectors: eight-element groups never straddle rows.
 inline bool vector_rows(const void* p, int64_t cols) { return cols % 8 == 0 && aligned_to(p, 16); }
 
