@@ -357,17 +357,50 @@ struct RowRing {
   }
 };
 
-// Two sums over the wpr warps of a row from the block's per-warp values.
-__device__ __forceinline__ float2 row_pair(const float (*red)[2], int first, int wpr) {
-  const float2 one = *reinterpret_cast<const float2*>(red[first]);
-  if (wpr == 1) return one;
-  F2 s = 0;
+// The rows' sums over the wpr warps that share them, from the block's per-warp
+// values: pairs (sum g, sum g h) of R rows.
+template <int R>
+__device__ __forceinline__ void row_sums(const float (*red)[2 * R], int first, int wpr, F2 (&s)[R]) {
+  if constexpr (R == 2) {
+    s[0] = s[1] = 0;
+#pragma unroll 4
+    for (int k = 0; k < wpr; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(red[first + k]);
+      s[0] = add2(s[0], f2(v.x, v.y));
+      s[1] = add2(s[1], f2(v.z, v.w));
+    }
+  } else {
+    s[0] = *reinterpret_cast<const F2*>(red[first]);
+    if (wpr == 1) return;
+    s[0] = 0;
 #pragma unroll 8
-  for (int k = 0; k < wpr; k += 2) {
-    const float4 v = *reinterpret_cast<const float4*>(red[first + k]);
-    s = add2(s, add2(f2(v.x, v.y), f2(v.z, v.w)));
+    for (int k = 0; k < wpr; k += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(red[first + k]);
+      s[0] = add2(s[0], add2(f2(v.x, v.y), f2(v.z, v.w)));
+    }
   }
-  return f2_get(s);
+}
+
+// A warp's sums of R rows (s[2 q]: sum g of row q, s[2 q + 1]: sum g h) over its
+// lanes, to `out`.  Halves, then quarters of the warp go on with a share of the
+// values each.
+template <int R>
+__device__ __forceinline__ void publish_sums(float (&s)[2 * R], float* out) {
+  const int lane = threadIdx.x & 31;
+  int own = 0;
+#pragma unroll
+  for (int n = 2 * R, o = 16; n > 1; n /= 2, o /= 2) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int k = 0; k < n / 2; ++k) {
+      const float give = upper ? s[k] : s[k + n / 2];
+      s[k] = (upper ? s[k + n / 2] : s[k]) + __shfl_xor_sync(kAll, give, o);
+    }
+    own = own * 2 + (upper ? 1 : 0);
+  }
+#pragma unroll
+  for (int o = 16 / (2 * R); o > 0; o >>= 1) s[0] += __shfl_xor_sync(kAll, s[0], o);
+  if ((lane & (32 / (2 * R) - 1)) == 0) out[own] = s[0];
 }
 
 // Each step of a block: its sums over step i + 1, then the gradients of step
@@ -375,18 +408,18 @@ __device__ __forceinline__ float2 row_pair(const float (*red)[2], int first, int
 // one barrier per step, with independent work on both sides of it.  A warp of
 // its own feeds the ring: its address arithmetic would otherwise hold up the
 // barrier of every step (2 us a step before, whatever the columns).
-template <typename T, typename W, int VEC, bool FUSED>
+template <typename T, typename W, int VEC, bool FUSED, int R>
 __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs a) {
   constexpr int G = kBwdGroups;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(16) float red[2][kBwdWarps][2];
+  __shared__ __align__(16) float red[2][kBwdWarps][2 * R];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
-  __shared__ float2 row_stats[kMaxStages][kBwdWarps];  // mean and rstd of a stage's rows
+  __shared__ float2 row_stats[kMaxStages][kBwdWarps * R];  // mean and rstd of a stage's rows
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int log = __ffs(a.wpr) - 1, part = warp & (a.wpr - 1), first = warp - part, slot = warp >> log;
-  const int rpi = kBwdWarps >> log;  // rows per step of the block
+  const int log = __ffs(a.wpr) - 1, part = warp & (a.wpr - 1), first = warp - part, slot = (warp >> log) * R;
+  const int rpi = (kBwdWarps >> log) * R;  // rows per step of the block
   const int64_t steps = (a.rows + rpi - 1) / rpi;
   const int mine = static_cast<int>((steps - blockIdx.x + gridDim.x - 1) / gridDim.x);
   const bool has_dz = FUSED && a.dz;
@@ -465,61 +498,82 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
       aw[g][p] = ab[g][p] = 0;
     }
   }
-  // This step's row and the next one's: where it is, its statistics and its
-  // place in the ring.
+  // The warp's rows (R neighbours) of this step and the next: the first one's
+  // number and element, their statistics and place in the ring.
   const int64_t stride = static_cast<int64_t>(gridDim.x) * rpi, stride_at = stride * a.cols;
-  struct Row {
-    int64_t row, at;  // row number, first element
-    uint32_t stage;  // its place in the ring
-    float mean, rstd;
+  struct Rows {
+    int64_t row, at;
+    uint32_t stage;
+    float mean[R], rstd[R];
   };
-  // The row's columns of tensor t in the ring (a stage starts at its first row).
-  const uint32_t slot_bytes = static_cast<uint32_t>(slot * a.cols * sizeof(T));
-  const auto row_in = [&](const Row& r, int t) {
+  // Row q's columns of tensor t in the ring (a stage starts at its first row).
+  const uint32_t row_bytes = static_cast<uint32_t>(a.cols * sizeof(T)), slot_bytes = slot * row_bytes;
+  const auto row_in = [&](const Rows& r, int q, int t) {
     const uint32_t shift = VEC ? 0u : ring_of[t].shift(r.at - static_cast<int64_t>(slot) * a.cols);
-    return r.stage + t * a.tensor_bytes + shift + slot_bytes;
+    return r.stage + t * a.tensor_bytes + shift + slot_bytes + q * row_bytes;
   };
   // 32-bit offsets from the array's name, so that the accesses stay shared-memory ones.
   const auto load_in = [&](uint32_t row, int c0) {
     return load_cols<VEC>(reinterpret_cast<const T*>(ring + row), c0, a.cols, lane);
   };
-  const auto sums = [&](Row& r, int s, float(*out)[2]) {
-    F2 s1 = 0, s2 = 0;
-    const float2 st = row_stats[s][slot];
-    r.mean = st.x;
-    r.rstd = st.y;
-    if (r.row < a.rows) {
-      const uint32_t dyr = row_in(r, 0), zr = row_in(r, 1);
-      const F2 nm = f2_all(-r.mean), rs = f2_all(r.rstd);
+  // A step of 256 columns: what one row adds to the sums ...
+  const auto add_up = [&](const Rows& r, int q, int g, int c0, F2& s1, F2& s2) {
+    const F2 nm = f2_all(-r.mean[q]), rs = f2_all(r.rstd[q]);
+    // columns past the end hold dY = 0 and add nothing
+    const Raw8<T> dy = load_in(row_in(r, q, 0), c0), z = load_in(row_in(r, q, 1), c0);
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int c0 = (part + g * a.wpr) * 256;
-        if (c0 < a.cols) {
-          // columns past the end hold dY = 0 and add nothing
-          const Raw8<T> dy = load_in(dyr, c0);
-          const Raw8<T> z = load_in(zr, c0);
+    for (int p = 0; p < 4; ++p) {
+      const F2 d = raw_f2(dy, p), h = mul2(add2(raw_f2(z, p), nm), rs), gr = mul2(d, w[g][p]);
+      aw[g][p] = fma2(d, h, aw[g][p]);
+      ab[g][p] = add2(ab[g][p], d);
+      s1 = add2(s1, gr);
+      s2 = fma2(gr, h, s2);
+    }
+  };
+  // ... and a row's gradients, from its two sums:
+  // rstd (dy w - s1 - h s2) = rstd dy w - rstd s1 - (z - mean) rstd^2 s2
+  const auto gradients = [&](const Rows& r, int q, int g, int c0, F2 k1, F2 k2) {
+    const F2 nm = f2_all(-r.mean[q]), rs = f2_all(r.rstd[q]);
+    const Raw8<T> dy = load_in(row_in(r, q, 0), c0), z = load_in(row_in(r, q, 1), c0);
+    F2 v[4];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const F2 d = raw_f2(dy, p), h = mul2(add2(raw_f2(z, p), nm), rs), gr = mul2(d, w[g][p]);
-            aw[g][p] = fma2(d, h, aw[g][p]);
-            ab[g][p] = add2(ab[g][p], d);
-            s1 = add2(s1, gr);
-            s2 = fma2(gr, h, s2);
-          }
-        }
+    for (int p = 0; p < 4; ++p) v[p] = fma2(mul2(raw_f2(dy, p), w[g][p]), rs, fma2(add2(raw_f2(z, p), nm), k2, k1));
+    if (has_dz) {
+      const Raw8<T> dz = load_in(row_in(r, q, 2), c0);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) v[p] = add2(v[p], raw_f2(dz, p));
+    }
+    store_grad<T, VEC, FUSED>(a, r.row + q, r.at + q * static_cast<int64_t>(a.cols), c0, lane, base, v);
+  };
+  // A step's rows into the sums; the warp's share of each row's two to `out`.
+  const auto first_pass = [&](Rows& r, int s, float* out) {
+    F2 t1[R], t2[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const float2 st = row_stats[s][slot + q];
+      r.mean[q] = st.x;
+      r.rstd[q] = st.y;
+      t1[q] = t2[q] = 0;
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int c0 = (part + g * a.wpr) * 256;
+      if (c0 < a.cols) {
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+          if (r.row + q < a.rows) add_up(r, q, g, c0, t1[q], t2[q]);
       }
     }
-    // Half of the warp goes on with the first sum, half with the second.
-    const float u = f2_sum(s1), v = f2_sum(s2);
-    const bool upper = lane & 16;
-    float keep = upper ? v : u;
-    keep += __shfl_xor_sync(kAll, upper ? u : v, 16);
+    float sum[2 * R];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) keep += __shfl_xor_sync(kAll, keep, o);
-    if ((lane & 15) == 0) out[warp][lane >> 4] = keep;
+    for (int q = 0; q < R; ++q) {
+      sum[2 * q] = f2_sum(t1[q]);
+      sum[2 * q + 1] = f2_sum(t2[q]);
+    }
+    publish_sums<R>(sum, out);
   };
 
-  Row cur, next;
+  Rows cur, next;
   next.row = static_cast<int64_t>(blockIdx.x) * rpi + slot;
   next.at = next.row * a.cols;
   next.stage = 0;
@@ -537,40 +591,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
   // The computing warps' own barrier.
   const auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kBwdWarps * 32) : "memory"); };
   mbar_wait(&full[0], 0, ctx);  // every block has a step
-  sums(next, 0, red[0]);
+  first_pass(next, 0, red[0][warp]);
   cur = next;
   advance();
   sync();
   int s_cur = 0;
   for (int i = 0; i < mine; ++i) {
-    const float2 sum = row_pair(red[i & 1], first, a.wpr);
+    F2 k1[R], k2[R];
+    {
+      F2 sum[R];
+      row_sums<R>(red[i & 1], first, a.wpr, sum);
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const float2 v = f2_get(sum[q]);
+        k1[q] = f2_all(-cur.rstd[q] * (v.x * a.inv_n));
+        k2[q] = f2_all(-cur.rstd[q] * (cur.rstd[q] * (v.y * a.inv_n)));
+      }
+    }
     if (i + 1 < mine) {
       mbar_wait(&full[s], parity, ctx);
-      sums(next, s, red[(i + 1) & 1]);
+      first_pass(next, s, red[(i + 1) & 1][warp]);
     }
-    if (cur.row < a.rows) {
-      // rstd (dy w - s1 - h s2) = rstd dy w - rstd s1 - (z - mean) rstd^2 s2
-      const F2 nm = f2_all(-cur.mean), rs = f2_all(cur.rstd);
-      const F2 k1 = f2_all(-cur.rstd * (sum.x * a.inv_n));
-      const F2 k2 = f2_all(-cur.rstd * (cur.rstd * (sum.y * a.inv_n)));
-      const uint32_t dyr = row_in(cur, 0), zr = row_in(cur, 1), dzr = row_in(cur, 2);
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int c0 = (part + g * a.wpr) * 256;
-        if (c0 < a.cols) {
-          const Raw8<T> dy = load_in(dyr, c0);
-          const Raw8<T> z = load_in(zr, c0);
-          F2 v[4];
+    for (int g = 0; g < G; ++g) {
+      const int c0 = (part + g * a.wpr) * 256;
+      if (c0 < a.cols) {
 #pragma unroll
-          for (int p = 0; p < 4; ++p)
-            v[p] = fma2(mul2(raw_f2(dy, p), w[g][p]), rs, fma2(add2(raw_f2(z, p), nm), k2, k1));
-          if (has_dz) {
-            const Raw8<T> dz = load_in(dzr, c0);
-#pragma unroll
-            for (int p = 0; p < 4; ++p) v[p] = add2(v[p], raw_f2(dz, p));
-          }
-          store_grad<T, VEC, FUSED>(a, cur.row, cur.at, c0, lane, base, v);
-        }
+        for (int q = 0; q < R; ++q)
+          if (cur.row + q < a.rows) gradients(cur, q, g, c0, k1[q], k2[q]);
       }
     }
     cur = next;
@@ -584,7 +632,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
   if (!a.part && !a.dw && !a.db) return;
   float* pw = a.part ? a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols : a.dw;
   float* pb = a.part ? pw + a.cols : a.db;
-  if (rpi == 1) {
+  const int slots = rpi / R, mine_slot = slot / R;
+  if (slots == 1) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int c0 = (part + g * a.wpr) * 256;
@@ -598,13 +647,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) ln_bwd_kernel(const LnBwdArgs 
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int c0 = (part + g * a.wpr) * 256;
-    store_pairs<VEC>(acc + (slot * 2) * a.cols, c0, a.cols, lane, aw[g]);
-    store_pairs<VEC>(acc + (slot * 2 + 1) * a.cols, c0, a.cols, lane, ab[g]);
+    store_pairs<VEC>(acc + (mine_slot * 2) * a.cols, c0, a.cols, lane, aw[g]);
+    store_pairs<VEC>(acc + (mine_slot * 2 + 1) * a.cols, c0, a.cols, lane, ab[g]);
   }
   sync();
   for (int c = threadIdx.x; c < 2 * a.cols; c += kBwdWarps * 32) {
     float sum = 0.0f;
-    for (int k = 0; k < rpi; ++k) sum += acc[k * 2 * a.cols + c];
+    for (int k = 0; k < slots; ++k) sum += acc[k * 2 * a.cols + c];
     if (c < a.cols) {
       if (pw) pw[c] = sum;
     } else if (pb) {
@@ -777,9 +826,9 @@ cudaError_t launch_ln_fwd(const LnFwdArgs& a, int32_t dtype, int32_t wdtype, boo
                          : launch_fwd_any<__half, float>(a, vec, fused, stream);
 }
 
-template <typename T, typename W, int VEC, bool FUSED>
+template <typename T, typename W, int VEC, bool FUSED, int R>
 cudaError_t launch_bwd_rows(const LnBwdArgs& a, int grid, size_t smem, cudaStream_t stream) {
-  auto kern = ln_bwd_kernel<T, W, VEC, FUSED>;
+  auto kern = ln_bwd_kernel<T, W, VEC, FUSED, R>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes));
   if (e != cudaSuccess) return e;
@@ -792,11 +841,24 @@ cudaError_t launch_bwd(LnBwdArgs a, bool vec, float* dw, float* db, cudaStream_t
   int blocks;
   cudaError_t e;
   a.wpr = warps_for(std::min(a.cols, kBwdCols), kBwdGroups);
-  const int rpi = kBwdWarps / a.wpr;
-  // Room for a stage's rows at any alignment.
-  a.tensor_bytes = static_cast<uint32_t>((static_cast<int64_t>(rpi) * std::min(a.cols, kBwdCols) * sizeof(T) + 15 + 127) / 128 * 128);
+  const int slots = kBwdWarps / a.wpr;
+  // Rows a warp takes per step: two halve the fixed cost of a step, where
+  // their stages still leave three in the ring and there are steps enough.
+  const auto plan = [&](int r) {
+    // Room for a stage's rows at any alignment.
+    const int64_t row_bytes = static_cast<int64_t>(std::min(a.cols, kBwdCols)) * sizeof(T);
+    a.tensor_bytes = static_cast<uint32_t>((slots * r * row_bytes + 15 + 127) / 128 * 128);
+    a.stages = static_cast<int>(
+        std::min<int64_t>(kMaxStages, kRingBytes / (static_cast<int64_t>(a.tensor_bytes) * (FUSED && a.dz ? 3 : 2))));
+  };
+  plan(2);
+  int rows_per_warp = 2;
+  if (a.stages < 3 || a.rows < static_cast<int64_t>(device_sm_count()) * slots * 4) {
+    rows_per_warp = 1;
+    plan(1);
+  }
+  const int rpi = slots * rows_per_warp;
   const int64_t stage = static_cast<int64_t>(a.tensor_bytes) * (FUSED && a.dz ? 3 : 2);
-  a.stages = static_cast<int>(std::min<int64_t>(kMaxStages, kRingBytes / stage));
   if (a.cols > kBwdCols || a.stages < 2) {
     ln_bwd_long_kernel<T, W, FUSED><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
     e = cudaGetLastError();
@@ -814,11 +876,18 @@ cudaError_t launch_bwd(LnBwdArgs a, bool vec, float* dw, float* db, cudaStream_t
       a.dw = dw;
       a.db = db;
     }
-    const size_t acc = static_cast<size_t>(rpi) * a.cols * 8;  // sums of the row slots
+    const size_t acc = static_cast<size_t>(slots) * a.cols * 8;  // sums of the row slots
     const size_t smem = std::max<size_t>(a.stages * stage, acc);
-    if (!vec) e = launch_bwd_rows<T, W, kRagged, FUSED>(a, blocks, smem, stream);
-    else if (aligned_layout(a.cols) == kWhole) e = launch_bwd_rows<T, W, kWhole, FUSED>(a, blocks, smem, stream);
-    else e = launch_bwd_rows<T, W, kAligned, FUSED>(a, blocks, smem, stream);
+    const int layout = vec ? aligned_layout(a.cols) : kRagged;
+    if (rows_per_warp == 2) {
+      if (layout == kRagged) e = launch_bwd_rows<T, W, kRagged, FUSED, 2>(a, blocks, smem, stream);
+      else if (layout == kWhole) e = launch_bwd_rows<T, W, kWhole, FUSED, 2>(a, blocks, smem, stream);
+      else e = launch_bwd_rows<T, W, kAligned, FUSED, 2>(a, blocks, smem, stream);
+    } else {
+      if (layout == kRagged) e = launch_bwd_rows<T, W, kRagged, FUSED, 1>(a, blocks, smem, stream);
+      else if (layout == kWhole) e = launch_bwd_rows<T, W, kWhole, FUSED, 1>(a, blocks, smem, stream);
+      else e = launch_bwd_rows<T, W, kAligned, FUSED, 1>(a, blocks, smem, stream);
+    }
   }
   if (e != cudaSuccess || !a.part) return e;
   const int v = a.cols % 4 == 0 ? 4 : 1;
