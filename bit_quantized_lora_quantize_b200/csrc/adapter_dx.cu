@@ -4,12 +4,13 @@
 //
 // A pass over dX: 4 bytes of HBM traffic per element against 4 r operations,
 // so it is HBM-bound at the ranks in use, and the register-fragment tensor
-// path (mma.sync) has room to spare.  A block takes a 128 x 128 tile; U enters
-// as its bf16 pair (hi + lo, about 16 significant bits), 64 ranks at a time.
+// path (mma.sync) has room to spare.  A block takes a 64 x 128 tile; U enters
+// as its bf16 pair (hi + lo, about 16 significant bits), 64 ranks at a time by
+// asynchronous copies, with the mask drawn while they are under way.
 //
 // The weight rows are handed to the tensor cores in an order that leaves each
 // lane with eight consecutive columns of dX: output column c of the 8-wide
-// block b of a 32-column group is column 8 (c / 2) + 2 b + c % 2 of the group.
+// block b of a warp's 32 columns is column 8 (c / 2) + 2 b + c % 2 of them.
 // So one 16-byte load, one Philox output and one 16-byte store serve a lane's
 // eight sums, straight from the accumulators.
 #include <cstdint>
@@ -24,10 +25,17 @@ namespace qlora {
 
 namespace {
 
-constexpr int kTile = 128;
-constexpr int kThreads = 256;  // 4 x 2 warps of 32 x 64
+constexpr int kTileM = 64;
+constexpr int kTileK = 128;
+constexpr int kThreads = 256;  // 2 x 4 warps of 32 x 32
 constexpr int kRanks = 64;     // ranks per step
-constexpr int kTileBytes = kTile * kRanks * 2;
+constexpr int kUBytes = kTileM * kRanks * 2;
+constexpr int kABytes = kTileK * kRanks * 2;
+
+// 16 bytes to shared memory; zeros when `in` is false (nothing is read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -53,51 +61,66 @@ __device__ __forceinline__ uint32_t a_offset(int row, int c) {
 __global__ void __launch_bounds__(kThreads, 2)
     adapter_dx_kernel(const uint16_t* __restrict__ U, const uint16_t* __restrict__ A, uint16_t* __restrict__ dX,
                       int64_t M, int64_t K, int r, int rp, const DropArgs d) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* s_hi = smem;
-  uint8_t* s_lo = smem + kTileBytes;
-  uint8_t* s_a = smem + 2 * kTileBytes;
+  __shared__ __align__(1024) uint8_t smem[2 * kUBytes + kABytes];
+  const uint32_t s_hi = smem_u32(smem), s_lo = s_hi + kUBytes, s_a = s_lo + kUBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wm = (warp & 3) * 32, wn = (warp >> 2) * 64;
-  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTile, m0 = static_cast<int64_t>(blockIdx.y) * kTile;
+  const int wm = (warp & 1) * 32, wn = (warp >> 1) * 32;
+  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTileK, m0 = static_cast<int64_t>(blockIdx.y) * kTileM;
+
+  const auto fetch = [&](int j0) {
+#pragma unroll
+    for (int t = 0; t < kTileM * 8 / kThreads; ++t) {
+      const int at = threadIdx.x + t * kThreads, row = at >> 3, c = at & 7;
+      const bool in = m0 + row < M;
+      const uint16_t* p = U + (in ? (m0 + row) * 2 * rp + j0 + c * 8 : 0);
+      copy16(s_hi + u_offset(row, c), p, in);
+      copy16(s_lo + u_offset(row, c), p + (in ? rp : 0), in);
+    }
+#pragma unroll
+    for (int t = 0; t < kTileK * 8 / kThreads; ++t) {
+      const int at = threadIdx.x + t * kThreads, row = at >> 3, c = at & 7;
+      const bool in = k0 + row < K && j0 + c * 8 < r;
+      copy16(s_a + a_offset(row, c), A + (in ? (k0 + row) * r + j0 + c * 8 : 0), in);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(0);
 
   // This lane's groups of eight: rows wm + 16 i + 8 h + lane / 4, columns
-  // wn + 32 g + 8 (lane % 4).  K % 64 == 0, so a group is whole or outside.
-  uint4 old[2][2][2];
+  // wn + 8 (lane % 4).  K % 64 == 0, so a group is whole or outside.
+  const int64_t k = k0 + wn + 8 * (lane & 3);
+  const uint64_t base = drop_base(d);
+  uint4 old[2][2];
+  KeepGroup keep[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      const int64_t m = m0 + wm + 16 * i + 8 * h + (lane >> 2);
+      if (m < M && k < K) old[i][h] = __ldcs(reinterpret_cast<const uint4*>(dX + m * K + k));
+    }
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int64_t m = m0 + wm + 16 * i + 8 * h + (lane >> 2), k = k0 + wn + 32 * g + 8 * (lane & 3);
-        if (m < M && k < K) old[i][h][g] = __ldcs(reinterpret_cast<const uint4*>(dX + m * K + k));
-      }
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t m = m0 + wm + 16 * i + 8 * h + (lane >> 2);
+      keep[i][h] = keep_group(d, base + m * d.groups + k / 8);
+    }
 
-  float acc[2][8][4];
+  float acc[2][4][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int b = 0; b < 8; ++b)
+    for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][b][e] = 0.0f;
 
   for (int j0 = 0; j0 < rp; j0 += kRanks) {
-    if (j0) __syncthreads();  // the previous step's fragments have been read
-#pragma unroll
-    for (int t = 0; t < kTile * 8 / kThreads; ++t) {
-      const int at = threadIdx.x + t * kThreads, row = at >> 3, c = at & 7;
-      uint4 hi = make_uint4(0, 0, 0, 0), lo = hi, a = hi;
-      if (m0 + row < M) {
-        const uint16_t* p = U + (m0 + row) * 2 * rp + j0 + c * 8;
-        hi = *reinterpret_cast<const uint4*>(p);
-        lo = *reinterpret_cast<const uint4*>(p + rp);
-      }
-      if (k0 + row < K && j0 + c * 8 < r) a = *reinterpret_cast<const uint4*>(A + (k0 + row) * r + j0 + c * 8);
-      *reinterpret_cast<uint4*>(s_hi + u_offset(row, c)) = hi;
-      *reinterpret_cast<uint4*>(s_lo + u_offset(row, c)) = lo;
-      *reinterpret_cast<uint4*>(s_a + a_offset(row, c)) = a;
+    if (j0) {
+      __syncthreads();  // the previous step's fragments have been read
+      fetch(j0);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 #pragma unroll
     for (int kk = 0; kk < kRanks / 16; ++kk) {
@@ -106,16 +129,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < 2; ++i) {
         // matrices: rows 0-7 and 8-15 of the first eight ranks, then of the next
         const int row = wm + 16 * i + (lane & 15), c = 2 * kk + (lane >> 4);
-        ldmatrix_x4(smem_u32(s_hi) + u_offset(row, c), uh[i]);
-        ldmatrix_x4(smem_u32(s_lo) + u_offset(row, c), ul[i]);
+        ldmatrix_x4(s_hi + u_offset(row, c), uh[i]);
+        ldmatrix_x4(s_lo + u_offset(row, c), ul[i]);
       }
 #pragma unroll
-      for (int bb = 0; bb < 4; ++bb) {
+      for (int bb = 0; bb < 2; ++bb) {
         // two 8-wide blocks: matrices (block 2 bb, ranks 0-7), (ranks 8-15), (block 2 bb + 1, ...)
         uint32_t w[4];
         const int b = 2 * bb + (lane >> 4), n = lane & 7;
-        const int row = wn + 32 * (b >> 2) + (n >> 1) * 8 + (b & 3) * 2 + (n & 1);
-        ldmatrix_x4(smem_u32(s_a) + a_offset(row, 2 * kk + ((lane >> 3) & 1)), w);
+        const int row = wn + (n >> 1) * 8 + b * 2 + (n & 1);
+        ldmatrix_x4(s_a + a_offset(row, 2 * kk + ((lane >> 3) & 1)), w);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           mma_bf16(acc[i][2 * bb], uh[i], w[0], w[1]);
@@ -127,48 +150,39 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
 
-  const uint64_t base = drop_base(d);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      const int64_t m = m0 + wm + 16 * i + 8 * h + (lane >> 2);
+      if (m >= M || k >= K) continue;
+      Raw8<__nv_bfloat16> x;
+      x.w[0] = old[i][h].x; x.w[1] = old[i][h].y; x.w[2] = old[i][h].z; x.w[3] = old[i][h].w;
+      float v[8];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int64_t m = m0 + wm + 16 * i + 8 * h + (lane >> 2), k = k0 + wn + 32 * g + 8 * (lane & 3);
-        if (m >= M || k >= K) continue;
-        const KeepGroup keep = keep_group(d, base + m * d.groups + k / 8);
-        Raw8<__nv_bfloat16> x;
-        x.w[0] = old[i][h][g].x; x.w[1] = old[i][h][g].y; x.w[2] = old[i][h][g].z; x.w[3] = old[i][h][g].w;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float add = acc[i][4 * g + (e >> 1)][2 * h + (e & 1)];
-          v[e] = raw_f32(x, e) + (keep(e) ? add : 0.0f);
-        }
-        store_group_stream(reinterpret_cast<__nv_bfloat16*>(dX) + m * K + k, raw_from<__nv_bfloat16>(v));
-      }
+      for (int e = 0; e < 8; ++e)
+        v[e] = raw_f32(x, e) + (keep[i][h](e) ? acc[i][e >> 1][2 * h + (e & 1)] : 0.0f);
+      store_group_stream(reinterpret_cast<__nv_bfloat16*>(dX) + m * K + k, raw_from<__nv_bfloat16>(v));
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_adapter_dx(const uint16_t* Upair, const uint16_t* A, uint16_t* dX, int64_t M, int64_t K, int r,
                               const DropArgs& d, cudaStream_t stream) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(adapter_dx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kTileBytes);
-  if (e != cudaSuccess) return e;
   // Row blocks beyond a grid's second dimension go to further launches.
   constexpr int64_t kMaxRowBlocks = 65535;
-  const int64_t row_blocks = (M + kTile - 1) / kTile;
+  const int64_t row_blocks = (M + kTileM - 1) / kTileM;
   for (int64_t b = 0; b < row_blocks; b += kMaxRowBlocks) {
-    const int64_t m0 = b * kTile;
+    const int64_t m0 = b * kTileM;
     DropArgs part = d;
     part.offset += static_cast<uint64_t>(m0) * d.groups;
-    const dim3 grid(static_cast<unsigned>((K + kTile - 1) / kTile),
+    const dim3 grid(static_cast<unsigned>((K + kTileK - 1) / kTileK),
                     static_cast<unsigned>(row_blocks - b < kMaxRowBlocks ? row_blocks - b : kMaxRowBlocks));
-    adapter_dx_kernel<<<grid, kThreads, 3 * kTileBytes, stream>>>(
-        Upair + m0 * 2 * lora_pad(r), A, dX + m0 * K, M - m0, K, r, lora_pad(r), part);
-    const cudaError_t le = cudaGetLastError();
-    if (le != cudaSuccess) return le;
+    adapter_dx_kernel<<<grid, kThreads, 0, stream>>>(Upair + m0 * 2 * lora_pad(r), A, dX + m0 * K, M - m0, K, r,
+                                                     lora_pad(r), part);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

@@ -36,11 +36,16 @@ inline qlora_status check_rows(int64_t rows, int64_t cols) {
 inline bool make_drop_args(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, int64_t cols,
                            DropArgs* d) {
   if (!(p >= 0.0 && p <= 1.0) || !aligned_to(offset_dev, 8)) return false;
-  d->seed = seed;
   d->offset = offset;
   d->offset_dev = offset_dev;
-  d->threshold = static_cast<uint32_t>(std::nearbyint(65536.0 * p));
-  d->gain = d->threshold < 65536u ? 65536.0f / static_cast<float>(65536u - d->threshold) : 0.0f;
+  for (uint32_t i = 0; i < 10; ++i) {
+    d->keys[i][0] = static_cast<uint32_t>(seed) + i * 0x9E3779B9u;
+    d->keys[i][1] = static_cast<uint32_t>(seed >> 32) + i * 0xBB67AE85u;
+  }
+  const uint32_t threshold = static_cast<uint32_t>(std::nearbyint(65536.0 * p));
+  d->above = (threshold << 16) - 1u;
+  d->all = threshold == 0;
+  d->gain = threshold < 65536u ? 65536.0f / static_cast<float>(65536u - threshold) : 0.0f;
   d->groups = (cols + 7) / 8;
   return true;
 }
