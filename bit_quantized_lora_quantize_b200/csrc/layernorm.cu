@@ -829,8 +829,8 @@ cudaError_t launch_ln_fwd(const LnFwdArgs& a, int32_t dtype, int32_t wdtype, boo
 template <typename T, typename W, int VEC, bool FUSED, int R>
 cudaError_t launch_bwd_rows(const LnBwdArgs& a, int grid, size_t smem, cudaStream_t stream) {
   auto kern = ln_bwd_kernel<T, W, VEC, FUSED, R>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_shared_memory(kern, kRingBytes, done);
   if (e != cudaSuccess) return e;
   kern<<<grid, kBwdThreads, smem, stream>>>(a);
   return cudaGetLastError();

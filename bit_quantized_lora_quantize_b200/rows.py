@@ -19,42 +19,58 @@ def _opt(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+_functions: dict = {}
+
+
 def _call(name: str, dev: torch.device, *args) -> None:
     """The library call `name` on the current stream of `dev`."""
-    f = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    index = dev.index
+    if index == _current_device():
+        status = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = f(*args, _raw_stream(index))
     if status:
         _check(name, status)
+
+
+# A small kernel runs for less time than torch.cuda.current_stream takes to
+# build its object: ask for the handle itself where torch has that call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _matrix(X: torch.Tensor):
     """(rows, cols, dtype code) of the tensor that sets a call's sizes."""
     if not X.is_cuda:
         raise ValueError("qlora kernels take CUDA tensors only (no CPU path)")
-    if X.dim() < 1 or not X.is_contiguous():
+    shape = X.shape
+    if not shape or not X.is_contiguous():
         raise ValueError("qlora kernels take contiguous tensors of at least one dimension")
     code = DTYPES.get(X.dtype)
     if code is None:
         raise ValueError("bfloat16, float16 or float32 tensors expected")
-    cols = X.shape[-1]
+    cols = shape[-1]
+    if len(shape) == 2:
+        return shape[0], cols, code
     return (X.numel() // cols if cols else 0), cols, code
 
 
 def _like(X: torch.Tensor, *ts: torch.Tensor | None) -> None:
     """Each tensor given matches X in shape, type and device and is contiguous."""
+    shape, dtype, dev = X.shape, X.dtype, X.device
     for t in ts:
-        if t is not None and (t.shape != X.shape or t.dtype != X.dtype or t.device != X.device
-                              or not t.is_contiguous()):
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous()):
             raise ValueError("contiguous tensors of one shape, type and device expected")
 
 
 def _vector(X: torch.Tensor, n: int, t: torch.Tensor | None, what: str, *dtypes: torch.dtype) -> None:
     """The vector, if there is one, has n values of one of these types, where X is."""
-    if t is not None and (t.numel() != n or t.dtype not in dtypes or t.device != X.device or not t.is_contiguous()):
+    if t is not None and (t.dtype not in dtypes or t.numel() != n or t.device != X.device or not t.is_contiguous()):
         raise ValueError(f"{what}: {n} contiguous values on the inputs' device expected, of a supported type")
 
 
@@ -83,9 +99,9 @@ def qlora_dropout_fwd(X: torch.Tensor, p: float, seed: int, offset: int = 0, res
     counters from `offset` (plus the value in the one-element int64 tensor
     `offset_dev`, read on the device)."""
     rows, cols, code = _matrix(X)
+    _like(X, residual, Y)
     if Y is None:
         Y = torch.empty_like(X)
-    _like(X, residual, Y)
     dev = _draws(X, seed, offset, offset_dev)
     _call("qlora_dropout_fwd", X.device, _ptr(X), _opt(residual), _ptr(Y), rows, cols, code, p, seed, offset, dev)
     return Y
@@ -95,9 +111,9 @@ def qlora_dropout_bwd(dY: torch.Tensor, p: float, seed: int, offset: int = 0, dX
                       offset_dev: torch.Tensor | None = None) -> torch.Tensor:
     """dX of the dropout drawn with the same p, seed and offset."""
     rows, cols, code = _matrix(dY)
+    _like(dY, dX)
     if dX is None:
         dX = torch.empty_like(dY)
-    _like(dY, dX)
     dev = _draws(dY, seed, offset, offset_dev)
     _call("qlora_dropout_bwd", dY.device, _ptr(dY), _ptr(dX), rows, cols, code, p, seed, offset, dev)
     return dX
@@ -125,7 +141,15 @@ def _norm_workspace(X: torch.Tensor, rows: int, cols: int, workspace: torch.Tens
     return workspace
 
 
+def _two(X: torch.Tensor, n: int):
+    """Two float32 vectors of n values."""
+    first = torch.empty(n, dtype=torch.float32, device=X.device)
+    return first, torch.empty_like(first)
+
+
 def _stats_out(X: torch.Tensor, rows: int, mean, rstd):
+    if mean is None and rstd is None:
+        return _two(X, rows)
     if mean is None:
         mean = torch.empty(rows, dtype=torch.float32, device=X.device)
     if rstd is None:
@@ -143,6 +167,8 @@ def _stats_in(X: torch.Tensor, rows: int, mean: torch.Tensor, rstd: torch.Tensor
 
 
 def _param_grads(X: torch.Tensor, cols: int, wanted: bool, dweight, dbias):
+    if wanted and dweight is None and dbias is None:
+        return _two(X, cols)
     if wanted and dweight is None:
         dweight = torch.empty(cols, dtype=torch.float32, device=X.device)
     if wanted and dbias is None:
@@ -161,7 +187,8 @@ def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bia
     wcode = _params(X, cols, weight, bias)
     if Y is None:
         Y = torch.empty_like(X)
-    _like(X, Y)
+    else:
+        _like(X, Y)
     mean, rstd = _stats_out(X, rows, mean, rstd)
     _call("qlora_layernorm_fwd", X.device, _ptr(X), _opt(weight), _opt(bias), _ptr(Y), _ptr(mean), _ptr(rstd), rows,
           cols, code, wcode, eps)
@@ -176,9 +203,9 @@ def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, r
     with ``param_grads=False`` unless their tensors are given."""
     rows, cols, code = _matrix(X)
     wcode = _params(X, cols, weight, None)
+    _like(X, dY, dX)
     if dX is None:
         dX = torch.empty_like(X)
-    _like(X, dY, dX)
     _stats_in(X, rows, mean, rstd)
     dweight, dbias = _param_grads(X, cols, param_grads, dweight, dbias)
     workspace = _norm_workspace(X, rows, cols, workspace)
@@ -195,11 +222,11 @@ def qlora_dropout_add_layernorm_fwd(X: torch.Tensor, residual: torch.Tensor, p: 
     """(Y, Z, mean, rstd): Z = residual + dropout(X) and its layer norm Y."""
     rows, cols, code = _matrix(X)
     wcode = _params(X, cols, weight, bias)
+    _like(X, residual, Y, Z)
     if Y is None:
         Y = torch.empty_like(X)
     if Z is None:
         Z = torch.empty_like(X)
-    _like(X, residual, Y, Z)
     mean, rstd = _stats_out(X, rows, mean, rstd)
     dev = _draws(X, seed, offset, offset_dev)
     _call("qlora_dropout_add_layernorm_fwd", X.device, _ptr(X), _ptr(residual), _opt(weight), _opt(bias), _ptr(Z),
@@ -217,11 +244,11 @@ def qlora_dropout_add_layernorm_bwd(dY: torch.Tensor, dZ: torch.Tensor | None, Z
     p, seed and offset; dZ is the gradient that reaches Z past the norm."""
     rows, cols, code = _matrix(Z)
     wcode = _params(Z, cols, weight, None)
+    _like(Z, dY, dZ, dX, dresidual)
     if dX is None:
         dX = torch.empty_like(Z)
     if dresidual is None:
         dresidual = torch.empty_like(Z)
-    _like(Z, dY, dZ, dX, dresidual)
     _stats_in(Z, rows, mean, rstd)
     dev = _draws(Z, seed, offset, offset_dev)
     dweight, dbias = _param_grads(Z, cols, param_grads, dweight, dbias)
@@ -268,7 +295,7 @@ def _linear(X: torch.Tensor, W: PackedNF4, A: torch.Tensor, B: torch.Tensor, wor
 
 
 def _typed(X: torch.Tensor, shape: tuple, dtype: torch.dtype, what: str, t: torch.Tensor) -> torch.Tensor:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != X.device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != X.device or not t.is_contiguous():
         raise ValueError(f"{what}: contiguous {dtype} of shape {tuple(shape)} on {X.device} expected")
     return t
 
