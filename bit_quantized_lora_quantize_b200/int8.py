@@ -10,7 +10,7 @@ from dataclasses import dataclass
 
 import torch
 
-from .qlora import QloraError, _ptr, lib
+from .qlora import QloraError, lib
 from .rows import DTYPES, _call, _matrix, _out, _typed
 
 
@@ -31,11 +31,12 @@ class PackedInt8:
 def _packed(X: torch.Tensor, p: PackedInt8, what: str):
     """(rows, cols, ld) of a packed matrix on X's device."""
     rows, cols = p.shape
-    c = p.codes
-    if c.dim() != 2 or c.shape[0] != rows or c.shape[1] < cols or c.dtype != torch.int8 or c.device != X.device \
+    c, s, dev = p.codes, p.scale, X.device
+    shape = c.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < cols or c.dtype != torch.int8 or c.device != dev \
             or c.stride(1) != 1:
-        raise ValueError(f"{what}.codes: int8 [{rows}, >= {cols}] with unit stride along rows expected on {X.device}")
-    _typed(X, (rows,), torch.float32, what + ".scale", p.scale)
+        raise ValueError(f"{what}.codes: int8 [{rows}, >= {cols}] with unit stride along rows expected on {dev}")
+    _typed(X, (rows,), torch.float32, what + ".scale", s)
     return rows, cols, p.ld
 
 
@@ -52,7 +53,7 @@ def qlora_quantize_int8(X: torch.Tensor, out: PackedInt8 | None = None) -> Packe
     elif tuple(out.shape) != (rows, cols) or out.codes.shape[1] < -(-cols // 16) * 16:
         raise ValueError("out does not hold a matrix of this shape")
     _, _, ld = _packed(X, out, "out")
-    _call("qlora_quantize_int8", X.device, _ptr(X), rows, cols, code, _ptr(out.codes), ld, _ptr(out.scale))
+    _call("qlora_quantize_int8", X.device, X.data_ptr(), rows, cols, code, out.codes.data_ptr(), ld, out.scale.data_ptr())
     return out
 
 
@@ -90,8 +91,8 @@ def qlora_matmul_int8(X: PackedInt8, W: PackedInt8, dtype: torch.dtype = torch.b
         raise ValueError("bfloat16, float16 or float32 results expected")
     workspace = _workspace(c, M, K, N, workspace)
     Y = _out(c, (M, N), dtype, "Y", Y)
-    _call("qlora_matmul_int8", c.device, _ptr(c), ldx, _ptr(X.scale), M, K, N, _ptr(W.codes), ldw, _ptr(W.scale),
-          _ptr(Y), DTYPES[dtype], _ptr(workspace), workspace.numel())
+    _call("qlora_matmul_int8", c.device, c.data_ptr(), ldx, X.scale.data_ptr(), M, K, N, W.codes.data_ptr(), ldw, W.scale.data_ptr(),
+          Y.data_ptr(), DTYPES[dtype], workspace.data_ptr(), workspace.numel())
     return Y
 
 
@@ -106,8 +107,8 @@ def qlora_linear_int8_fwd(X: torch.Tensor, W: PackedInt8, workspace: torch.Tenso
         raise ValueError("W: [N, K] for inputs [M, K] expected")
     workspace = _workspace(X, M, K, N, workspace)
     Y = _out(X, (M, N), X.dtype, "Y", Y)
-    _call("qlora_linear_int8_fwd", X.device, _ptr(X), M, K, N, code, _ptr(W.codes), ldw, _ptr(W.scale), _ptr(Y),
-          _ptr(workspace), workspace.numel())
+    _call("qlora_linear_int8_fwd", X.device, X.data_ptr(), M, K, N, code, W.codes.data_ptr(), ldw, W.scale.data_ptr(), Y.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return Y
 
 

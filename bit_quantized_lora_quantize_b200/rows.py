@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from .qlora import PackedNF4, QloraError, _check, _ptr, lib, packed_sizes
+from .qlora import PackedNF4, QloraError, _check, lib, packed_sizes
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -75,13 +75,17 @@ def _vector(X: torch.Tensor, n: int, t: torch.Tensor | None, what: str, *dtypes:
 
 
 def _params(X: torch.Tensor, cols: int, weight, bias) -> int:
-    """Type code of the norm's parameters."""
-    _vector(X, cols, weight, "weight", X.dtype, torch.float32)
-    _vector(X, cols, bias, "bias", X.dtype, torch.float32)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError("weight and bias of one type expected")
+    """Type code of the norm's parameters: X's type or float32, one for both."""
     given = weight if weight is not None else bias
-    return DTYPES[X.dtype if given is None else given.dtype]
+    if given is None:
+        return DTYPES[X.dtype]
+    dtype, dev = given.dtype, X.device
+    if dtype != X.dtype and dtype != torch.float32:
+        raise ValueError("weight and bias: the inputs' type or float32 expected")
+    for t in (weight, bias):
+        if t is not None and (t.dtype != dtype or t.numel() != cols or t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"weight and bias: {cols} contiguous values of one type on the inputs' device expected")
+    return DTYPES[dtype]
 
 
 def _draws(X: torch.Tensor, seed: int, offset: int, offset_dev: torch.Tensor | None) -> int | None:
@@ -103,7 +107,7 @@ def qlora_dropout_fwd(X: torch.Tensor, p: float, seed: int, offset: int = 0, res
     if Y is None:
         Y = torch.empty_like(X)
     dev = _draws(X, seed, offset, offset_dev)
-    _call("qlora_dropout_fwd", X.device, _ptr(X), _opt(residual), _ptr(Y), rows, cols, code, p, seed, offset, dev)
+    _call("qlora_dropout_fwd", X.device, X.data_ptr(), _opt(residual), Y.data_ptr(), rows, cols, code, p, seed, offset, dev)
     return Y
 
 
@@ -115,7 +119,7 @@ def qlora_dropout_bwd(dY: torch.Tensor, p: float, seed: int, offset: int = 0, dX
     if dX is None:
         dX = torch.empty_like(dY)
     dev = _draws(dY, seed, offset, offset_dev)
-    _call("qlora_dropout_bwd", dY.device, _ptr(dY), _ptr(dX), rows, cols, code, p, seed, offset, dev)
+    _call("qlora_dropout_bwd", dY.device, dY.data_ptr(), dX.data_ptr(), rows, cols, code, p, seed, offset, dev)
     return dX
 
 
@@ -141,9 +145,15 @@ def _norm_workspace(X: torch.Tensor, rows: int, cols: int, workspace: torch.Tens
     return workspace
 
 
+# torch.empty_strided takes two thirds of torch.empty's time on the host, and
+# short calls are bound by that.
+def _vector_of(dev: torch.device, n: int) -> torch.Tensor:
+    return torch.empty_strided((n,), (1,), dtype=torch.float32, device=dev)
+
+
 def _two(X: torch.Tensor, n: int):
     """Two float32 vectors of n values."""
-    first = torch.empty(n, dtype=torch.float32, device=X.device)
+    first = _vector_of(X.device, n)
     return first, torch.empty_like(first)
 
 
@@ -151,9 +161,9 @@ def _stats_out(X: torch.Tensor, rows: int, mean, rstd):
     if mean is None and rstd is None:
         return _two(X, rows)
     if mean is None:
-        mean = torch.empty(rows, dtype=torch.float32, device=X.device)
+        mean = _vector_of(X.device, rows)
     if rstd is None:
-        rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
+        rstd = _vector_of(X.device, rows)
     _vector(X, rows, mean, "mean", torch.float32)
     _vector(X, rows, rstd, "rstd", torch.float32)
     return mean, rstd
@@ -170,9 +180,9 @@ def _param_grads(X: torch.Tensor, cols: int, wanted: bool, dweight, dbias):
     if wanted and dweight is None and dbias is None:
         return _two(X, cols)
     if wanted and dweight is None:
-        dweight = torch.empty(cols, dtype=torch.float32, device=X.device)
+        dweight = _vector_of(X.device, cols)
     if wanted and dbias is None:
-        dbias = torch.empty(cols, dtype=torch.float32, device=X.device)
+        dbias = _vector_of(X.device, cols)
     _vector(X, cols, dweight, "dweight", torch.float32)
     _vector(X, cols, dbias, "dbias", torch.float32)
     return dweight, dbias
@@ -190,7 +200,7 @@ def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bia
     else:
         _like(X, Y)
     mean, rstd = _stats_out(X, rows, mean, rstd)
-    _call("qlora_layernorm_fwd", X.device, _ptr(X), _opt(weight), _opt(bias), _ptr(Y), _ptr(mean), _ptr(rstd), rows,
+    _call("qlora_layernorm_fwd", X.device, X.data_ptr(), _opt(weight), _opt(bias), Y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), rows,
           cols, code, wcode, eps)
     return Y, mean, rstd
 
@@ -209,8 +219,8 @@ def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, r
     _stats_in(X, rows, mean, rstd)
     dweight, dbias = _param_grads(X, cols, param_grads, dweight, dbias)
     workspace = _norm_workspace(X, rows, cols, workspace)
-    _call("qlora_layernorm_bwd", X.device, _ptr(dY), _ptr(X), _ptr(mean), _ptr(rstd), _opt(weight), _ptr(dX),
-          _opt(dweight), _opt(dbias), rows, cols, code, wcode, _ptr(workspace), workspace.numel())
+    _call("qlora_layernorm_bwd", X.device, dY.data_ptr(), X.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _opt(weight), dX.data_ptr(),
+          _opt(dweight), _opt(dbias), rows, cols, code, wcode, workspace.data_ptr(), workspace.numel())
     return dX, dweight, dbias
 
 
@@ -229,8 +239,8 @@ def qlora_dropout_add_layernorm_fwd(X: torch.Tensor, residual: torch.Tensor, p: 
         Z = torch.empty_like(X)
     mean, rstd = _stats_out(X, rows, mean, rstd)
     dev = _draws(X, seed, offset, offset_dev)
-    _call("qlora_dropout_add_layernorm_fwd", X.device, _ptr(X), _ptr(residual), _opt(weight), _opt(bias), _ptr(Z),
-          _ptr(Y), _ptr(mean), _ptr(rstd), rows, cols, code, wcode, eps, p, seed, offset, dev)
+    _call("qlora_dropout_add_layernorm_fwd", X.device, X.data_ptr(), residual.data_ptr(), _opt(weight), _opt(bias), Z.data_ptr(),
+          Y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), rows, cols, code, wcode, eps, p, seed, offset, dev)
     return Y, Z, mean, rstd
 
 
@@ -253,9 +263,9 @@ def qlora_dropout_add_layernorm_bwd(dY: torch.Tensor, dZ: torch.Tensor | None, Z
     dev = _draws(Z, seed, offset, offset_dev)
     dweight, dbias = _param_grads(Z, cols, param_grads, dweight, dbias)
     workspace = _norm_workspace(Z, rows, cols, workspace)
-    _call("qlora_dropout_add_layernorm_bwd", Z.device, _ptr(dY), _opt(dZ), _ptr(Z), _ptr(mean), _ptr(rstd),
-          _opt(weight), _ptr(dX), _ptr(dresidual), _opt(dweight), _opt(dbias), rows, cols, code, wcode, p, seed,
-          offset, dev, _ptr(workspace), workspace.numel())
+    _call("qlora_dropout_add_layernorm_bwd", Z.device, dY.data_ptr(), _opt(dZ), Z.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+          _opt(weight), dX.data_ptr(), dresidual.data_ptr(), _opt(dweight), _opt(dbias), rows, cols, code, wcode, p, seed,
+          offset, dev, workspace.data_ptr(), workspace.numel())
     return dX, dresidual, dweight, dbias
 
 
@@ -279,29 +289,35 @@ def _linear(X: torch.Tensor, W: PackedNF4, A: torch.Tensor, B: torch.Tensor, wor
     if X.dim() != 2 or len(W.shape) != 2 or A.dim() != 2 or B.dim() != 2:
         raise ValueError("matrices expected")
     (M, K), N, r = X.shape, W.shape[0], A.shape[1]
-    _typed(X, (M, K), torch.bfloat16, "X", X)
-    _typed(X, (K, r), torch.bfloat16, "A", A)
-    _typed(X, (r, N), torch.bfloat16, "B", B)
-    nc, nb, nb2 = packed_sizes(N * K)
-    _typed(X, (nc,), torch.uint8, "W.codes", W.codes)
-    _typed(X, (nb,), torch.uint8, "W.absmax_q", W.absmax_q)
-    _typed(X, (nb2 + (W.dq == "centred_fp8"),), torch.float32, "W.absmax_scale", W.absmax_scale)
     if W.shape[1] != K:
         raise ValueError("W: [N, K] for inputs [M, K] expected")
     if workspace is None:
         workspace = new_dropout_workspace(M, K, N, r, X.device)
-    _typed(X, (workspace.numel(),), torch.uint8, "workspace", workspace)
+    nc, nb, nb2 = packed_sizes(N * K)
+    bf16, u8 = torch.bfloat16, torch.uint8
+    _all_typed(X.device, ((X, (M, K), bf16, "X"), (A, (K, r), bf16, "A"), (B, (r, N), bf16, "B"),
+                          (W.codes, (nc,), u8, "W.codes"), (W.absmax_q, (nb,), u8, "W.absmax_q"),
+                          (W.absmax_scale, (nb2 + (W.dq == "centred_fp8"),), torch.float32, "W.absmax_scale"),
+                          (workspace, (workspace.numel(),), u8, "workspace")))
     return M, K, N, r, workspace
 
 
+def _all_typed(dev: torch.device, given) -> None:
+    """Each (tensor, shape, type, name) is as it says, contiguous and on `dev`."""
+    for t, shape, dtype, what in given:
+        if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{what}: contiguous {dtype} of shape {tuple(shape)} on {dev} expected")
+
+
 def _typed(X: torch.Tensor, shape: tuple, dtype: torch.dtype, what: str, t: torch.Tensor) -> torch.Tensor:
-    if t.shape != shape or t.dtype != dtype or t.device != X.device or not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous {dtype} of shape {tuple(shape)} on {X.device} expected")
+    _all_typed(X.device, ((t, shape, dtype, what),))
     return t
 
 
 def _out(X: torch.Tensor, shape: tuple, dtype: torch.dtype, what: str, t: torch.Tensor | None) -> torch.Tensor:
-    return torch.empty(shape, dtype=dtype, device=X.device) if t is None else _typed(X, shape, dtype, what, t)
+    if t is None:
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=X.device)
+    return _typed(X, shape, dtype, what, t)
 
 
 def qlora_linear_fwd_dropout(X: torch.Tensor, W: PackedNF4, A: torch.Tensor, B: torch.Tensor, scale: float, p: float,
@@ -314,9 +330,9 @@ def qlora_linear_fwd_dropout(X: torch.Tensor, W: PackedNF4, A: torch.Tensor, B: 
     Y = _out(X, (M, N), torch.bfloat16, "Y", Y)
     T_save = _out(X, (M, r), torch.float32, "T_save", T_save)
     dev = _draws(X, seed, offset, offset_dev)
-    _call("qlora_linear_fwd_dropout", X.device, _ptr(X), M, K, N, _ptr(W.codes), _ptr(W.absmax_q),
-          _ptr(W.absmax_scale), W.code_value, _ptr(A), _ptr(B), r, scale, p, seed, offset, dev, _ptr(Y), _ptr(T_save),
-          _ptr(workspace), workspace.numel())
+    _call("qlora_linear_fwd_dropout", X.device, X.data_ptr(), M, K, N, W.codes.data_ptr(), W.absmax_q.data_ptr(),
+          W.absmax_scale.data_ptr(), W.code_value, A.data_ptr(), B.data_ptr(), r, scale, p, seed, offset, dev, Y.data_ptr(), T_save.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return Y, T_save
 
 
@@ -327,15 +343,14 @@ def qlora_linear_bwd_dropout(dY: torch.Tensor, X: torch.Tensor, T_save: torch.Te
                              offset_dev: torch.Tensor | None = None):
     """(dX, dA, dB) of the forward drawn with the same p, seed and offset."""
     M, K, N, r, workspace = _linear(X, W, A, B, workspace)
-    _typed(X, (M, N), torch.bfloat16, "dY", dY)
-    _typed(X, (M, r), torch.float32, "T_save", T_save)
+    _all_typed(X.device, ((dY, (M, N), torch.bfloat16, "dY"), (T_save, (M, r), torch.float32, "T_save")))
     dX = _out(X, (M, K), torch.bfloat16, "dX", dX)
     dA = _out(X, (K, r), torch.float32, "dA", dA)
     dB = _out(X, (r, N), torch.float32, "dB", dB)
     dev = _draws(X, seed, offset, offset_dev)
-    _call("qlora_linear_bwd_dropout", X.device, _ptr(dY), _ptr(X), _ptr(T_save), M, K, N, _ptr(W.codes),
-          _ptr(W.absmax_q), _ptr(W.absmax_scale), W.code_value, _ptr(A), _ptr(B), r, scale, p, seed, offset, dev,
-          _ptr(dX), _ptr(dA), _ptr(dB), _ptr(workspace), workspace.numel())
+    _call("qlora_linear_bwd_dropout", X.device, dY.data_ptr(), X.data_ptr(), T_save.data_ptr(), M, K, N, W.codes.data_ptr(),
+          W.absmax_q.data_ptr(), W.absmax_scale.data_ptr(), W.code_value, A.data_ptr(), B.data_ptr(), r, scale, p, seed, offset, dev,
+          dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(), workspace.numel())
     return dX, dA, dB
 
 
