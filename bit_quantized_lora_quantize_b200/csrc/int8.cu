@@ -160,8 +160,10 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf, int warp,
   return __reduce_max_sync(kAll, buf[first + (lane & (wpr - 1))]);
 }
 
+// Three blocks of 16 warps per SM where rows take four steps: 300 rows of 11003
+// need no second wave (10.1 -> 7.0 us).
 template <typename T, int G, int VEC>
-__global__ void __launch_bounds__(1024) quantize_rows_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(G == 1 ? 1024 : 512, G == 1 || sizeof(T) == 4 ? 2 : 3) quantize_rows_kernel(const QuantArgs a) {
   griddep_launch_dependents();  // a product that follows may load its weight meanwhile
   __shared__ uint32_t red[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(1024) quantize_long_rows_kernel(const QuantArg
 
 template <typename T>
 cudaError_t launch_quantize_rows(QuantArgs a, cudaStream_t stream) {
-  if (a.cols > 32 * 256 * kQuantGroups) {
+  if (a.cols > 16 * 256 * kQuantGroups) {
     quantize_long_rows_kernel<T><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
     return cudaGetLastError();
   }
