@@ -6,7 +6,7 @@
 // so it is HBM-bound at the ranks in use, and the register-fragment tensor
 // path (mma.sync) has room to spare.  A block takes a 64 x 128 tile; U enters
 // as its bf16 pair (hi + lo, about 16 significant bits), 64 ranks at a time by
-// asynchronous copies, with the mask drawn while they are under way.
+// asynchronous copies.
 //
 // The weight rows are handed to the tensor cores in an order that leaves each
 // lane with eight consecutive columns of dX: output column c of the 8-wide
@@ -58,7 +58,7 @@ __device__ __forceinline__ uint32_t a_offset(int row, int c) {
   return row * 128 + ((c ^ (((row >> 3) & 3) * 2 + (row & 1))) << 4);
 }
 
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     adapter_dx_kernel(const uint16_t* __restrict__ U, const uint16_t* __restrict__ A, uint16_t* __restrict__ dX,
                       int64_t M, int64_t K, int r, int rp, const DropArgs d) {
   __shared__ __align__(1024) uint8_t smem[2 * kUBytes + kABytes];
@@ -67,45 +67,30 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int wm = (warp & 1) * 32, wn = (warp >> 1) * 32;
   const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTileK, m0 = static_cast<int64_t>(blockIdx.y) * kTileM;
 
+  // Thread t copies 16-byte chunk t % 8 of rows t / 8, t / 8 + 32, ...
+  const int crow = threadIdx.x >> 3, chunk = threadIdx.x & 7;
+  const int rows_m = static_cast<int>(min(static_cast<int64_t>(kTileM), M - m0));
+  const int rows_k = static_cast<int>(min(static_cast<int64_t>(kTileK), K - k0));
+  const uint16_t* u_src = U + (m0 + crow) * 2 * rp + chunk * 8;
+  const uint16_t* a_src = A + (k0 + crow) * r + chunk * 8;
   const auto fetch = [&](int j0) {
 #pragma unroll
-    for (int t = 0; t < kTileM * 8 / kThreads; ++t) {
-      const int at = threadIdx.x + t * kThreads, row = at >> 3, c = at & 7;
-      const bool in = m0 + row < M;
-      const uint16_t* p = U + (in ? (m0 + row) * 2 * rp + j0 + c * 8 : 0);
-      copy16(s_hi + u_offset(row, c), p, in);
-      copy16(s_lo + u_offset(row, c), p + (in ? rp : 0), in);
+    for (int t = 0; t < kTileM / 32; ++t) {
+      const int row = crow + t * 32;
+      const bool in = row < rows_m;
+      const uint16_t* p = in ? u_src + t * 64 * rp + j0 : U;
+      copy16(s_hi + u_offset(row, chunk), p, in);
+      copy16(s_lo + u_offset(row, chunk), p + (in ? rp : 0), in);
     }
 #pragma unroll
-    for (int t = 0; t < kTileK * 8 / kThreads; ++t) {
-      const int at = threadIdx.x + t * kThreads, row = at >> 3, c = at & 7;
-      const bool in = k0 + row < K && j0 + c * 8 < r;
-      copy16(s_a + a_offset(row, c), A + (in ? (k0 + row) * r + j0 + c * 8 : 0), in);
+    for (int t = 0; t < kTileK / 32; ++t) {
+      const int row = crow + t * 32;
+      const bool in = row < rows_k && j0 + chunk * 8 < r;
+      copy16(s_a + a_offset(row, chunk), in ? a_src + t * 32 * r + j0 : A, in);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   fetch(0);
-
-  // This lane's groups of eight: rows wm + 16 i + 8 h + lane / 4, columns
-  // wn + 8 (lane % 4).  K % 64 == 0, so a group is whole or outside.
-  const int64_t k = k0 + wn + 8 * (lane & 3);
-  const uint64_t base = drop_base(d);
-  uint4 old[2][2];
-  KeepGroup keep[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t m = m0 + wm + 16 * i + 8 * h + (lane >> 2);
-      if (m < M && k < K) old[i][h] = __ldcs(reinterpret_cast<const uint4*>(dX + m * K + k));
-    }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t m = m0 + wm + 16 * i + 8 * h + (lane >> 2);
-      keep[i][h] = keep_group(d, base + m * d.groups + k / 8);
-    }
 
   float acc[2][4][4];
 #pragma unroll
@@ -150,19 +135,36 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
 
+  // This lane's groups of eight: rows wm + 16 i + 8 h + lane / 4, columns
+  // wn + 8 (lane % 4).  K % 64 == 0, so a group is whole or outside.  Three
+  // blocks per SM hide these loads and the draws better than registers held
+  // for them across the products did (4096 x 8192 at rank 64: 49 us, 57 with
+  // two blocks).
+  const int64_t k = k0 + wn + 8 * (lane & 3);
+  const int row0 = wm + (lane >> 2);
+  if (k >= K) return;
+  uint16_t* at = dX + (m0 + row0) * K + k;
+  uint64_t counter = drop_base(d) + (m0 + row0) * d.groups + k / 8;
+  const int64_t step = 8 * K, steps = 8 * d.groups;
+  uint4 old[2][2];
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+    if (row0 + 8 * n < rows_m) old[n >> 1][n & 1] = __ldcs(reinterpret_cast<const uint4*>(at + n * step));
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t m = m0 + wm + 16 * i + 8 * h + (lane >> 2);
-      if (m >= M || k >= K) continue;
-      Raw8<__nv_bfloat16> x;
-      x.w[0] = old[i][h].x; x.w[1] = old[i][h].y; x.w[2] = old[i][h].z; x.w[3] = old[i][h].w;
-      float v[8];
+      if (row0 + 16 * i + 8 * h < rows_m) {
+        const KeepGroup keep = keep_group(d, counter);
+        Raw8<__nv_bfloat16> x;
+        x.w[0] = old[i][h].x; x.w[1] = old[i][h].y; x.w[2] = old[i][h].z; x.w[3] = old[i][h].w;
+        float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = raw_f32(x, e) + (keep[i][h](e) ? acc[i][e >> 1][2 * h + (e & 1)] : 0.0f);
-      store_group_stream(reinterpret_cast<__nv_bfloat16*>(dX) + m * K + k, raw_from<__nv_bfloat16>(v));
+        for (int e = 0; e < 8; ++e) v[e] = raw_f32(x, e) + (keep(e) ? acc[i][e >> 1][2 * h + (e & 1)] : 0.0f);
+        store_group_stream(reinterpret_cast<__nv_bfloat16*>(at), raw_from<__nv_bfloat16>(v));
+      }
+      at += step;
+      counter += steps;
     }
 }
 
