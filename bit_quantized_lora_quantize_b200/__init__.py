@@ -5,8 +5,9 @@ The product is the C-ABI library ``libqlora.so`` (include/qlora.h) built from
 ``csrc/`` by ``build.py``; ``qlora`` is its thin Python binding and
 ``synthetic`` the seeded input generator used by tests and the benchmark;
 ``rows`` the binding of the row-wise operators around the linears (dropout,
-layer norm), ``int8`` that of the linear on 8-bit integer weights, ``dp`` the data-parallel gradient bucket and ``paged`` the paged AdamW of the
-adapters.
+layer norm, the linear with adapter dropout), ``int8`` that of the linear on
+8-bit integer weights, ``dp`` the data-parallel gradient bucket and ``paged``
+the paged AdamW of the adapters.
 """
 
 from .qlora import (  # noqa: F401

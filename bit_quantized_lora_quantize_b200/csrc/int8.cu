@@ -163,7 +163,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf, int warp,
 // Three blocks of 16 warps per SM where rows take four steps: 300 rows of 11003
 // need no second wave (10.1 -> 7.0 us).
 template <typename T, int G, int VEC>
-__global__ void __launch_bounds__(G == 1 ? 1024 : 512, G == 1 || sizeof(T) == 4 ? 2 : 3) quantize_rows_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(G == 1 ? 1024 : 512, G == 1 || sizeof(T) == 4 ? 2 : 3)
+    quantize_rows_kernel(const QuantArgs a) {
   griddep_launch_dependents();  // a product that follows may load its weight meanwhile
   __shared__ uint32_t red[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -438,8 +439,8 @@ __device__ __forceinline__ void load_scales(const PairGemmArgs& a, int col0, int
 // 32 columns of a warp's 32 rows of Y from their whole-number sums; `sw` holds
 // the columns' scales.
 template <typename T>
-__device__ __forceinline__ void store_scaled(const PairGemmArgs& a, int row, int col0, const uint32_t (&v)[32], float sx,
-                                             const float* sw, float* turn) {
+__device__ __forceinline__ void store_scaled(const PairGemmArgs& a, int row, int col0, const uint32_t (&v)[32],
+                                             float sx, const float* sw, float* turn) {
   const int lane = threadIdx.x & 31;
   float f[32];
 #pragma unroll
@@ -873,7 +874,8 @@ qlora_status qlora_linear_int8_fwd(const void* X, int64_t M, int64_t K, int64_t 
   float* scale = reinterpret_cast<float*>(ws + l.scale);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(st, "linear_int8_fwd", 2);
-  cudaError_t e = launch_quantize_int8(dtype, QuantArgs{X, codes, scale, M, padded_depth(K), static_cast<int>(K), 1}, st);
+  const QuantArgs quant{X, codes, scale, M, padded_depth(K), static_cast<int>(K), 1};
+  cudaError_t e = launch_quantize_int8(dtype, quant, st);
   if (e == cudaSuccess)
     e = launch_matmul_int8(dtype, codes, padded_depth(K), scale, M, K, N, Wq, ldw, w_scale, Y, ws, true, st);
   prof.done();

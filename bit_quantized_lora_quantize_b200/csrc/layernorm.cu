@@ -824,7 +824,8 @@ cudaError_t launch_fwd_any(const LnFwdArgs& a, bool vec, bool fused, cudaStream_
 
 cudaError_t launch_ln_fwd(const LnFwdArgs& a, int32_t dtype, int32_t wdtype, bool fused, cudaStream_t stream) {
   const bool vec = vector_rows(a.x, a.cols) && vector_rows(a.y, a.cols) && vector_rows(a.w, a.cols) &&
-                   vector_rows(a.b, a.cols) && (!fused || (vector_rows(a.residual, a.cols) && vector_rows(a.z, a.cols)));
+                   vector_rows(a.b, a.cols) &&
+                   (!fused || (vector_rows(a.residual, a.cols) && vector_rows(a.z, a.cols)));
   if (dtype == QLORA_DTYPE_FP32) return launch_fwd_any<float, float>(a, vec, fused, stream);
   if (dtype == QLORA_DTYPE_BF16)
     return wdtype == dtype ? launch_fwd_any<__nv_bfloat16, __nv_bfloat16>(a, vec, fused, stream)

@@ -25,7 +25,8 @@ class PackedInt8:
 
     @property
     def ld(self) -> int:
-        return self.codes.stride(0) if self.codes.shape[0] > 1 else self.codes.shape[1]
+        # a single row has no next one to lie at a stride
+        return self.codes.stride(0) if self.codes.shape[0] > 1 else -(-self.codes.shape[1] // 16) * 16
 
 
 def _packed(X: torch.Tensor, p: PackedInt8, what: str):
@@ -53,7 +54,8 @@ def qlora_quantize_int8(X: torch.Tensor, out: PackedInt8 | None = None) -> Packe
     elif tuple(out.shape) != (rows, cols) or out.codes.shape[1] < -(-cols // 16) * 16:
         raise ValueError("out does not hold a matrix of this shape")
     _, _, ld = _packed(X, out, "out")
-    _call("qlora_quantize_int8", X.device, X.data_ptr(), rows, cols, code, out.codes.data_ptr(), ld, out.scale.data_ptr())
+    _call("qlora_quantize_int8", X.device, X.data_ptr(), rows, cols, code, out.codes.data_ptr(), ld,
+          out.scale.data_ptr())
     return out
 
 
@@ -91,8 +93,8 @@ def qlora_matmul_int8(X: PackedInt8, W: PackedInt8, dtype: torch.dtype = torch.b
         raise ValueError("bfloat16, float16 or float32 results expected")
     workspace = _workspace(c, M, K, N, workspace)
     Y = _out(c, (M, N), dtype, "Y", Y)
-    _call("qlora_matmul_int8", c.device, c.data_ptr(), ldx, X.scale.data_ptr(), M, K, N, W.codes.data_ptr(), ldw, W.scale.data_ptr(),
-          Y.data_ptr(), DTYPES[dtype], workspace.data_ptr(), workspace.numel())
+    _call("qlora_matmul_int8", c.device, c.data_ptr(), ldx, X.scale.data_ptr(), M, K, N, W.codes.data_ptr(), ldw,
+          W.scale.data_ptr(), Y.data_ptr(), DTYPES[dtype], workspace.data_ptr(), workspace.numel())
     return Y
 
 
@@ -107,8 +109,8 @@ def qlora_linear_int8_fwd(X: torch.Tensor, W: PackedInt8, workspace: torch.Tenso
         raise ValueError("W: [N, K] for inputs [M, K] expected")
     workspace = _workspace(X, M, K, N, workspace)
     Y = _out(X, (M, N), X.dtype, "Y", Y)
-    _call("qlora_linear_int8_fwd", X.device, X.data_ptr(), M, K, N, code, W.codes.data_ptr(), ldw, W.scale.data_ptr(), Y.data_ptr(),
-          workspace.data_ptr(), workspace.numel())
+    _call("qlora_linear_int8_fwd", X.device, X.data_ptr(), M, K, N, code, W.codes.data_ptr(), ldw, W.scale.data_ptr(),
+          Y.data_ptr(), workspace.data_ptr(), workspace.numel())
     return Y
 
 

@@ -107,7 +107,8 @@ def qlora_dropout_fwd(X: torch.Tensor, p: float, seed: int, offset: int = 0, res
     if Y is None:
         Y = torch.empty_like(X)
     dev = _draws(X, seed, offset, offset_dev)
-    _call("qlora_dropout_fwd", X.device, X.data_ptr(), _opt(residual), Y.data_ptr(), rows, cols, code, p, seed, offset, dev)
+    _call("qlora_dropout_fwd", X.device, X.data_ptr(), _opt(residual), Y.data_ptr(), rows, cols, code, p, seed,
+          offset, dev)
     return Y
 
 
@@ -200,8 +201,8 @@ def qlora_layernorm_fwd(X: torch.Tensor, weight: torch.Tensor | None = None, bia
     else:
         _like(X, Y)
     mean, rstd = _stats_out(X, rows, mean, rstd)
-    _call("qlora_layernorm_fwd", X.device, X.data_ptr(), _opt(weight), _opt(bias), Y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), rows,
-          cols, code, wcode, eps)
+    _call("qlora_layernorm_fwd", X.device, X.data_ptr(), _opt(weight), _opt(bias), Y.data_ptr(), mean.data_ptr(),
+          rstd.data_ptr(), rows, cols, code, wcode, eps)
     return Y, mean, rstd
 
 
@@ -219,8 +220,9 @@ def qlora_layernorm_bwd(dY: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, r
     _stats_in(X, rows, mean, rstd)
     dweight, dbias = _param_grads(X, cols, param_grads, dweight, dbias)
     workspace = _norm_workspace(X, rows, cols, workspace)
-    _call("qlora_layernorm_bwd", X.device, dY.data_ptr(), X.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _opt(weight), dX.data_ptr(),
-          _opt(dweight), _opt(dbias), rows, cols, code, wcode, workspace.data_ptr(), workspace.numel())
+    _call("qlora_layernorm_bwd", X.device, dY.data_ptr(), X.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+          _opt(weight), dX.data_ptr(), _opt(dweight), _opt(dbias), rows, cols, code, wcode, workspace.data_ptr(),
+          workspace.numel())
     return dX, dweight, dbias
 
 
@@ -239,8 +241,9 @@ def qlora_dropout_add_layernorm_fwd(X: torch.Tensor, residual: torch.Tensor, p: 
         Z = torch.empty_like(X)
     mean, rstd = _stats_out(X, rows, mean, rstd)
     dev = _draws(X, seed, offset, offset_dev)
-    _call("qlora_dropout_add_layernorm_fwd", X.device, X.data_ptr(), residual.data_ptr(), _opt(weight), _opt(bias), Z.data_ptr(),
-          Y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), rows, cols, code, wcode, eps, p, seed, offset, dev)
+    _call("qlora_dropout_add_layernorm_fwd", X.device, X.data_ptr(), residual.data_ptr(), _opt(weight), _opt(bias),
+          Z.data_ptr(), Y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), rows, cols, code, wcode, eps, p, seed, offset,
+          dev)
     return Y, Z, mean, rstd
 
 
@@ -263,9 +266,9 @@ def qlora_dropout_add_layernorm_bwd(dY: torch.Tensor, dZ: torch.Tensor | None, Z
     dev = _draws(Z, seed, offset, offset_dev)
     dweight, dbias = _param_grads(Z, cols, param_grads, dweight, dbias)
     workspace = _norm_workspace(Z, rows, cols, workspace)
-    _call("qlora_dropout_add_layernorm_bwd", Z.device, dY.data_ptr(), _opt(dZ), Z.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-          _opt(weight), dX.data_ptr(), dresidual.data_ptr(), _opt(dweight), _opt(dbias), rows, cols, code, wcode, p, seed,
-          offset, dev, workspace.data_ptr(), workspace.numel())
+    _call("qlora_dropout_add_layernorm_bwd", Z.device, dY.data_ptr(), _opt(dZ), Z.data_ptr(), mean.data_ptr(),
+          rstd.data_ptr(), _opt(weight), dX.data_ptr(), dresidual.data_ptr(), _opt(dweight), _opt(dbias), rows, cols,
+          code, wcode, p, seed, offset, dev, workspace.data_ptr(), workspace.numel())
     return dX, dresidual, dweight, dbias
 
 
@@ -331,8 +334,8 @@ def qlora_linear_fwd_dropout(X: torch.Tensor, W: PackedNF4, A: torch.Tensor, B: 
     T_save = _out(X, (M, r), torch.float32, "T_save", T_save)
     dev = _draws(X, seed, offset, offset_dev)
     _call("qlora_linear_fwd_dropout", X.device, X.data_ptr(), M, K, N, W.codes.data_ptr(), W.absmax_q.data_ptr(),
-          W.absmax_scale.data_ptr(), W.code_value, A.data_ptr(), B.data_ptr(), r, scale, p, seed, offset, dev, Y.data_ptr(), T_save.data_ptr(),
-          workspace.data_ptr(), workspace.numel())
+          W.absmax_scale.data_ptr(), W.code_value, A.data_ptr(), B.data_ptr(), r, scale, p, seed, offset, dev,
+          Y.data_ptr(), T_save.data_ptr(), workspace.data_ptr(), workspace.numel())
     return Y, T_save
 
 
@@ -348,9 +351,10 @@ def qlora_linear_bwd_dropout(dY: torch.Tensor, X: torch.Tensor, T_save: torch.Te
     dA = _out(X, (K, r), torch.float32, "dA", dA)
     dB = _out(X, (r, N), torch.float32, "dB", dB)
     dev = _draws(X, seed, offset, offset_dev)
-    _call("qlora_linear_bwd_dropout", X.device, dY.data_ptr(), X.data_ptr(), T_save.data_ptr(), M, K, N, W.codes.data_ptr(),
-          W.absmax_q.data_ptr(), W.absmax_scale.data_ptr(), W.code_value, A.data_ptr(), B.data_ptr(), r, scale, p, seed, offset, dev,
-          dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _call("qlora_linear_bwd_dropout", X.device, dY.data_ptr(), X.data_ptr(), T_save.data_ptr(), M, K, N,
+          W.codes.data_ptr(), W.absmax_q.data_ptr(), W.absmax_scale.data_ptr(), W.code_value, A.data_ptr(),
+          B.data_ptr(), r, scale, p, seed, offset, dev, dX.data_ptr(), dA.data_ptr(), dB.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return dX, dA, dB
 
 

@@ -116,7 +116,8 @@ def test_deepest_sums_stay_exact(M, N):
     assert abs(float(Y.max()) - 127 * 127 * K) <= 128
 
 
-@pytest.mark.parametrize("M,K,N", [(1, 1000, 512), (7, 4096, 4096), (100, 555, 300), (400, 1024, 768), (150, 999, 1001)])
+@pytest.mark.parametrize("M,K,N", [(1, 1000, 512), (7, 4096, 4096), (100, 555, 300), (400, 1024, 768),
+                                   (150, 999, 1001)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_linear_from_floats(M, K, N, dtype):
     t = TYPES[dtype]
@@ -142,6 +143,15 @@ def test_a_bad_token_stays_alone():
         assert got[3].isnan().all()
         keep = torch.arange(M) != 3
         assert torch.equal(got[keep], clean[keep])
+
+
+def test_single_rows_need_no_stride():
+    """One row of codes of any length: there is no next row to be apart from."""
+    X, xq, sx = packed(1, 777, 2)
+    W, wq, sw = packed(1, 777, 4)
+    for M_codes, N_codes in ((X.codes[:, :777], W.codes[:, :777]), (X.codes, W.codes)):
+        Y = q.qlora_matmul_int8(q.PackedInt8(M_codes, X.scale, (1, 777)), q.PackedInt8(N_codes, W.scale, (1, 777)))
+        check(Y, matmul_int8(xq, sx, wq, sw))
 
 
 def test_one_workspace_for_several_sizes():

@@ -136,7 +136,8 @@ def fwd_bounds(x, w, b, y, mean, rstd, dtype, cols):
     return out_err(y, ey, dtype), 1.01 * em + 1e-40, 1.01 * rel * rstd
 
 
-FWD = [(1, 1), (3, 8), (5, 31), (2, 256), (9, 257), (300, 250), (40, 1000), (301, 1024), (300, 2048), (299, 768), (7, 2304), (310, 6400), (1, 4096),
+FWD = [(1, 1), (3, 8), (5, 31), (2, 256), (9, 257), (300, 250), (40, 1000), (301, 1024), (300, 2048), (299, 768), (7, 2304),
+       (310, 6400), (1, 4096),
        (300, 4096), (37, 5003), (1, 8192), (310, 8192), (300, 11008), (4, 22016), (300, 32768), (3, 32776),
        (2, 40001)]
 
@@ -217,7 +218,8 @@ def bwd_bounds(dy, x, mean, rstd, w, dx, rows, cols, dtype, extra=None):
 
 
 BWD = [(1, 1), (3, 8), (17, 31), (16, 256), (50, 257), (700, 250), (40, 1000), (2500, 1024), (333, 4096), (1, 8192),
-       (60, 768), (33, 2304), (9, 2560), (20, 6400), (777, 5003), (700, 8192), (5, 8200), (130, 11008), (3, 22016), (2, 40001)]
+       (60, 768), (33, 2304), (9, 2560), (20, 6400), (777, 5003), (700, 8192), (5, 8200),
+       (130, 11008), (3, 22016), (2, 40001)]
 
 
 @pytest.mark.parametrize("rows,cols", BWD)
