@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -92,18 +93,23 @@ struct LnFwdArgs {
   int cols;
   float eps, inv_n;
   int wpr;
-  DropArgs drop;
 };
+
+// The draws' constants, only where there are draws.
+struct NoDrop {};
+template <bool FUSED>
+using FwdDrop = std::conditional_t<FUSED, DropArgs, NoDrop>;
+
 
 // Values of one lane's eight columns after the residual dropout, rounded to
 // T and stored to Z.
 template <typename T, int VEC>
-__device__ __forceinline__ Raw8<T> add_dropped(const LnFwdArgs& a, int64_t row, int c0, int lane, uint64_t base,
+__device__ __forceinline__ Raw8<T> add_dropped(const LnFwdArgs& a, const DropArgs& drop, int64_t row, int c0, int lane, uint64_t base,
                                                const Raw8<T>& x, const Raw8<T>& r) {
-  const auto keep = keep_cols<VEC>(a.drop, base + row * a.drop.groups + c0 / 8, lane);
+  const auto keep = keep_cols<VEC>(drop, base + row * drop.groups + c0 / 8, lane);
   float v[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = keep(e) ? fmaf(raw_f32(x, e), a.drop.gain, raw_f32(r, e)) : raw_f32(r, e);
+  for (int e = 0; e < 8; ++e) v[e] = keep(e) ? fmaf(raw_f32(x, e), drop.gain, raw_f32(r, e)) : raw_f32(r, e);
   const Raw8<T> z = raw_from<T>(v);
   store_cols<VEC>(static_cast<T*>(a.z) + row * a.cols, c0, a.cols, lane, z);
   return z;
@@ -152,7 +158,7 @@ __device__ __forceinline__ void normalise(const LnFwdArgs& a, int64_t row, int c
 }
 
 template <typename T, typename W, int G, int VEC, bool FUSED>
-__global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kernel(const LnFwdArgs a) {
+__global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kernel(const LnFwdArgs a, const FwdDrop<FUSED> drop) {
   __shared__ float red[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = warp & (a.wpr - 1), first = warp - part, shift = __ffs(a.wpr) - 1;
@@ -170,13 +176,14 @@ __global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kern
       if constexpr (FUSED) r[g] = load_cols<VEC>(rr, c0, a.cols, lane);
     }
   }
-  const uint64_t base = FUSED ? drop_base(a.drop) : 0;
+  uint64_t base = 0;
+  if constexpr (FUSED) base = drop_base(drop);
   F2 v[G][4];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int c0 = (part + g * a.wpr) * 256;
     if (valid && c0 < a.cols) {
-      if constexpr (FUSED) x[g] = add_dropped<T, VEC>(a, row, c0, lane, base, x[g], r[g]);
+      if constexpr (FUSED) x[g] = add_dropped<T, VEC>(a, drop, row, c0, lane, base, x[g], r[g]);
       raw_pairs(x[g], v[g]);
       s += group_sum(v[g]);
     }
@@ -204,17 +211,18 @@ __global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kern
 // Rows too long for the registers of a block: three passes, the later ones
 // mostly from L2.
 template <typename T, typename W, int VEC, bool FUSED>
-__global__ void __launch_bounds__(1024) ln_fwd_long_kernel(const LnFwdArgs a) {
+__global__ void __launch_bounds__(1024) ln_fwd_long_kernel(const LnFwdArgs a, const FwdDrop<FUSED> drop) {
   __shared__ float red[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x;
   const T* xr = static_cast<const T*>(a.x) + row * a.cols;
-  const uint64_t base = FUSED ? drop_base(a.drop) : 0;
+  uint64_t base = 0;
+  if constexpr (FUSED) base = drop_base(drop);
   float s = 0.0f;
   for (int c0 = warp * 256; c0 < a.cols; c0 += 32 * 256) {
     Raw8<T> x = load_cols<VEC>(xr, c0, a.cols, lane);
     if constexpr (FUSED)
-      x = add_dropped<T, VEC>(a, row, c0, lane, base, x,
+      x = add_dropped<T, VEC>(a, drop, row, c0, lane, base, x,
                                 load_cols<VEC>(static_cast<const T*>(a.residual) + row * a.cols, c0, a.cols, lane));
     F2 v[4];
     raw_pairs(x, v);
@@ -789,10 +797,10 @@ int warps_for(int64_t cols, int groups) {
 }
 
 template <typename T, typename W, int VEC, bool FUSED>
-cudaError_t launch_fwd(LnFwdArgs a, cudaStream_t stream) {
+cudaError_t launch_fwd(LnFwdArgs a, const FwdDrop<FUSED>& drop, cudaStream_t stream) {
   if (a.cols > kFwdWarps * 256 * kFwdMaxGroups) {
     constexpr int kLong = VEC == kRagged ? kRagged : kAligned;
-    ln_fwd_long_kernel<T, W, kLong, FUSED><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
+    ln_fwd_long_kernel<T, W, kLong, FUSED><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a, drop);
     return cudaGetLastError();
   }
   // Few rows: one step per warp where 32 warps allow it, for latency.
@@ -804,34 +812,36 @@ cudaError_t launch_fwd(LnFwdArgs a, cudaStream_t stream) {
   const int warps = std::max(a.wpr, 4);
   const int64_t rpb = warps / a.wpr;
   const unsigned grid = static_cast<unsigned>((a.rows + rpb - 1) / rpb);
-  if (groups == 1) ln_fwd_kernel<T, W, 1, VEC, FUSED><<<grid, warps * 32, 0, stream>>>(a);
-  else if (groups == 2) ln_fwd_kernel<T, W, 2, VEC, FUSED><<<grid, warps * 32, 0, stream>>>(a);
-  else ln_fwd_kernel<T, W, 4, VEC, FUSED><<<grid, warps * 32, 0, stream>>>(a);
+  if (groups == 1) ln_fwd_kernel<T, W, 1, VEC, FUSED><<<grid, warps * 32, 0, stream>>>(a, drop);
+  else if (groups == 2) ln_fwd_kernel<T, W, 2, VEC, FUSED><<<grid, warps * 32, 0, stream>>>(a, drop);
+  else ln_fwd_kernel<T, W, 4, VEC, FUSED><<<grid, warps * 32, 0, stream>>>(a, drop);
   return cudaGetLastError();
 }
 
 template <typename T, typename W, bool FUSED>
-cudaError_t launch_fwd_layout(const LnFwdArgs& a, bool vec, cudaStream_t stream) {
-  if (!vec) return launch_fwd<T, W, kRagged, FUSED>(a, stream);
-  return aligned_layout(a.cols) == kWhole ? launch_fwd<T, W, kWhole, FUSED>(a, stream)
-                                          : launch_fwd<T, W, kAligned, FUSED>(a, stream);
+cudaError_t launch_fwd_layout(const LnFwdArgs& a, const FwdDrop<FUSED>& drop, bool vec, cudaStream_t stream) {
+  if (!vec) return launch_fwd<T, W, kRagged, FUSED>(a, drop, stream);
+  return aligned_layout(a.cols) == kWhole ? launch_fwd<T, W, kWhole, FUSED>(a, drop, stream)
+                                          : launch_fwd<T, W, kAligned, FUSED>(a, drop, stream);
 }
 
 template <typename T, typename W>
-cudaError_t launch_fwd_any(const LnFwdArgs& a, bool vec, bool fused, cudaStream_t stream) {
-  return fused ? launch_fwd_layout<T, W, true>(a, vec, stream) : launch_fwd_layout<T, W, false>(a, vec, stream);
+cudaError_t launch_fwd_any(const LnFwdArgs& a, const DropArgs* drop, bool vec, cudaStream_t stream) {
+  return drop ? launch_fwd_layout<T, W, true>(a, *drop, vec, stream)
+              : launch_fwd_layout<T, W, false>(a, NoDrop{}, vec, stream);
 }
 
-cudaError_t launch_ln_fwd(const LnFwdArgs& a, int32_t dtype, int32_t wdtype, bool fused, cudaStream_t stream) {
+cudaError_t launch_ln_fwd(const LnFwdArgs& a, const DropArgs* drop, int32_t dtype, int32_t wdtype,
+                          cudaStream_t stream) {
   const bool vec = vector_rows(a.x, a.cols) && vector_rows(a.y, a.cols) && vector_rows(a.w, a.cols) &&
                    vector_rows(a.b, a.cols) &&
-                   (!fused || (vector_rows(a.residual, a.cols) && vector_rows(a.z, a.cols)));
-  if (dtype == QLORA_DTYPE_FP32) return launch_fwd_any<float, float>(a, vec, fused, stream);
+                   (!drop || (vector_rows(a.residual, a.cols) && vector_rows(a.z, a.cols)));
+  if (dtype == QLORA_DTYPE_FP32) return launch_fwd_any<float, float>(a, drop, vec, stream);
   if (dtype == QLORA_DTYPE_BF16)
-    return wdtype == dtype ? launch_fwd_any<__nv_bfloat16, __nv_bfloat16>(a, vec, fused, stream)
-                           : launch_fwd_any<__nv_bfloat16, float>(a, vec, fused, stream);
-  return wdtype == dtype ? launch_fwd_any<__half, __half>(a, vec, fused, stream)
-                         : launch_fwd_any<__half, float>(a, vec, fused, stream);
+    return wdtype == dtype ? launch_fwd_any<__nv_bfloat16, __nv_bfloat16>(a, drop, vec, stream)
+                           : launch_fwd_any<__nv_bfloat16, float>(a, drop, vec, stream);
+  return wdtype == dtype ? launch_fwd_any<__half, __half>(a, drop, vec, stream)
+                         : launch_fwd_any<__half, float>(a, drop, vec, stream);
 }
 
 template <typename T, typename W, int VEC, bool FUSED, int R>
@@ -936,8 +946,8 @@ qlora_status check_types(int32_t dtype, int32_t wdtype) {
 
 size_t ln_workspace_bytes(int64_t cols) { return kLnStatusBytes + static_cast<size_t>(kBwdMaxBlocks) * 2 * cols * 4; }
 
-qlora_status fwd_call(LnFwdArgs& a, int64_t rows, int64_t cols, int32_t dtype, int32_t wdtype, float eps, bool fused,
-                      const char* name, void* stream) {
+qlora_status fwd_call(LnFwdArgs& a, const DropArgs* drop, int64_t rows, int64_t cols, int32_t dtype, int32_t wdtype,
+                      float eps, const char* name, void* stream) {
   qlora_status s = check_types(dtype, wdtype);
   if (s == QLORA_OK) s = check_rows(rows, cols);
   if (s != QLORA_OK) return s;
@@ -952,7 +962,7 @@ qlora_status fwd_call(LnFwdArgs& a, int64_t rows, int64_t cols, int32_t dtype, i
   a.inv_n = static_cast<float>(1.0 / static_cast<double>(cols));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(st, name, 1);
-  const cudaError_t e = launch_ln_fwd(a, dtype, wdtype, fused, st);
+  const cudaError_t e = launch_ln_fwd(a, drop, dtype, wdtype, st);
   prof.done();
   return e == cudaSuccess ? QLORA_OK : cuda_fail(e);
 }
@@ -1001,7 +1011,7 @@ qlora_status qlora_layernorm_fwd(const void* X, const void* weight, const void* 
   a.y = Y;
   a.mean = mean;
   a.rstd = rstd;
-  return fwd_call(a, rows, cols, dtype, wdtype, eps, false, "layernorm_fwd", stream);
+  return fwd_call(a, nullptr, rows, cols, dtype, wdtype, eps, "layernorm_fwd", stream);
 }
 
 qlora_status qlora_dropout_add_layernorm_fwd(const void* X, const void* residual, const void* weight,
@@ -1011,7 +1021,8 @@ qlora_status qlora_dropout_add_layernorm_fwd(const void* X, const void* residual
                                              void* stream) {
   if (!X || !residual || !Z || !Y || !(p >= 0.0 && p <= 1.0)) return QLORA_ERR_INVALID_ARG;
   LnFwdArgs a{};
-  if (!make_drop_args(p, seed, offset, offset_dev, cols, &a.drop)) return QLORA_ERR_ALIGNMENT;
+  DropArgs drop;
+  if (!make_drop_args(p, seed, offset, offset_dev, cols, &drop)) return QLORA_ERR_ALIGNMENT;
   a.x = X;
   a.residual = residual;
   a.w = weight;
@@ -1020,7 +1031,7 @@ qlora_status qlora_dropout_add_layernorm_fwd(const void* X, const void* residual
   a.y = Y;
   a.mean = mean;
   a.rstd = rstd;
-  return fwd_call(a, rows, cols, dtype, wdtype, eps, true, "dropout_add_layernorm_fwd", stream);
+  return fwd_call(a, &drop, rows, cols, dtype, wdtype, eps, "dropout_add_layernorm_fwd", stream);
 }
 
 size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols) {
