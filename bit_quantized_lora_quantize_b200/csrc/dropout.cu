@@ -3,10 +3,13 @@
 // The mask is a function of (seed, counter) alone, so the backward pass draws
 // it again and it is never stored: a training step moves the activations and
 // nothing else.  One 128-bit Philox output serves eight elements with 16 bits
-// each: about 100 integer instructions per group of eight, half of what the
-// SMs can issue in the time HBM needs to move the group in bf16.  Elementwise
-// and HBM-bound: each thread loads its groups first and draws while the loads
-// are in flight; float32 arithmetic, one rounding per output.
+// each: about 100 instructions per group of eight with the rest of the work,
+// two thirds of what the SMs can issue in the time HBM needs to move the group
+// in bf16.  Elementwise and HBM-bound: each thread loads its groups first and
+// draws while the loads are in flight; float32 arithmetic, one rounding per
+// output.  Measured: 8192 x 11008 in bf16 55.4 us = 6.5 TB/s, 0.99 of the
+// measured copy bandwidth; ragged rows by scalar accesses (777 x 5003 in fp16)
+// 7.7 us, twice the time of 777 x 5000.
 //
 // Dropped elements are selected away, not multiplied by zero: an infinity or
 // a NaN there leaves no trace.

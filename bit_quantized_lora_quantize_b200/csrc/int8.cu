@@ -8,15 +8,21 @@
 // depth and no order of work changes a result; float32 enters in the epilogue.
 //
 // Three kernels:
-// - quantization: one pass, rows in registers, HBM-bound;
+// - quantization: one pass, rows in registers, HBM-bound (4096 x 8192 in bf16
+//   20.5 us, 0.75 of the copy bandwidth);
 // - up to 16 tokens, bound by reading the weight: `token_kernel` streams it
-//   straight into the register fragments of mma.sync;
+//   straight into the register fragments of mma.sync (one token, 8192 x 8192:
+//   15.5 us of which 10.3 are the weight at the copy bandwidth; 22016 x 8192:
+//   35.4 us, 0.78 of it);
 // - more tokens: `pair_kernel`, CTA pairs (cta_group::2) with 256 x 256 tiles
 //   fed by a TMA ring; persistent, with two accumulators in TMEM so that a
-//   tile's epilogue runs under the next tile's products, or, where there are
-//   too few tiles for the SMs, two or four pairs of a cluster on each tile.
-//   (A narrower tile does not help: a tcgen05.mma over 128 rows per SM costs
-//   about the same for 16 columns as for 256.)
+//   tile's epilogue runs under the next tile's products (4096 x 8192 x 8192:
+//   177 us, 3.1 P operations/s; tensor pipe 83 % busy), or, where the tiles
+//   fill less than half of the SMs, several pairs to a tile, each a part of
+//   the depth (300 x 11003 x 4099: 30.3 us).
+//   Narrower tiles do not help: a tcgen05.mma over 128 rows per SM costs about
+//   the same for 16 columns as for 256 (8192 x 8192 with one token on that
+//   path: 24.8 us).
 #include <algorithm>
 #include <cstdint>
 #include <cuda.h>
@@ -710,8 +716,10 @@ cudaError_t launch_pair_gemm(const CUtensorMap& x, const CUtensorMap& w, const P
 }
 
 // Pairs per tile.  A 128-deep block takes a pair about 0.33 us and handing
-// over and adding partial sums about 7 us (200 tokens on 8192 rows: 26.2 us
-// with two pairs at a depth of 8192, 28.3 with one; 15.8 against 11.6 at 2048).
+// over and adding partial sums about 7 us.  Measured with the split chosen here
+// against one pair a tile: 64 x 8192 x 8192 21.8 against 24.9 us, 300 x 11003 x
+// 4099 30.3 against 39.2, 200 x 8192 x 8192 26.2 against 26.7; a depth of 2048
+// stays with one (15.8 us with two, 11.7 with one).
 int pair_split(int64_t tiles, int nkb, int sms) {
   const int pairs = std::min(std::max(1, sms / 2), kMaxPairs);
   int best = 1;

@@ -26,6 +26,13 @@
 // added by a second, small kernel in a fixed order, so results are the same
 // from run to run.  Rows of over 8192 columns take one block each and a second
 // pass for the parameters.
+//
+// Measured on 4096 x 8192, as a fraction of the copy bandwidth: forward 28.7 us
+// (0.71) in bf16 and 48.8 (0.84) in float32, fused 48.1 (0.85) and 95.4 (0.86);
+// backward 46.2 (0.66) and 68.6 (0.90), fused 70.9 (0.72) and 109 (0.94).  In
+// float32 HBM is the bound; in bf16 the instructions per element are (about 23
+// in the backward, 12 of them arithmetic on pairs, 6 unpacking), and the
+// forward's loads wait for the block's reductions before them.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
