@@ -9,7 +9,7 @@
 // draws while the loads are in flight; float32 arithmetic, one rounding per
 // output.  Measured: 8192 x 11008 in bf16 55.4 us = 6.5 TB/s, 0.99 of the
 // measured copy bandwidth; ragged rows by scalar accesses (777 x 5003 in fp16)
-// 7.7 us, twice the time of 777 x 5000.
+// 6.4 us, against 4.1 of 777 x 5000.
 //
 // Dropped elements are selected away, not multiplied by zero: an infinity or
 // a NaN there leaves no trace.
@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(kDropThreads)
   const int lane = threadIdx.x & 31;
   const int64_t chunk = static_cast<int64_t>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5);
   if (chunk >= nchunks) return;
-  const int64_t row = chunk / chunks_per_row;
+  // (a 64-bit division takes as many instructions as a draw)
+  const int64_t row = nchunks >> 32 ? chunk / chunks_per_row
+                                    : static_cast<uint32_t>(chunk) / static_cast<uint32_t>(chunks_per_row);
   const int c0 = static_cast<int>(chunk - row * chunks_per_row) * 256;
   const int64_t at = row * cols;
   const Raw8<T> x = load_cols<kRagged>(X + at, c0, cols, lane);

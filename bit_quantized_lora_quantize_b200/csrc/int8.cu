@@ -9,7 +9,8 @@
 //
 // Three kernels:
 // - quantization: one pass, rows in registers, HBM-bound (4096 x 8192 in bf16
-//   20.5 us, 0.75 of the copy bandwidth);
+//   20.4 us, 0.75 of the copy bandwidth; ragged, by scalar accesses, 4096 x 8191
+//   30.6 us);
 // - up to 16 tokens, bound by reading the weight: `token_kernel` streams it
 //   straight into the register fragments of mma.sync (one token, 8192 x 8192:
 //   15.5 us of which 10.3 are the weight at the copy bandwidth; 22016 x 8192:
@@ -149,10 +150,15 @@ __device__ __forceinline__ void store_codes(const QuantArgs& a, int64_t row, int
           make_uint2(prmt(prmt(k[0], k[1], 0x0040), prmt(k[2], k[3], 0x0040), 0x5410),
                      prmt(prmt(k[4], k[5], 0x0040), prmt(k[6], k[7], 0x0040), 0x5410));
   } else {
+    int8_t* p = out + (c0 + lane);
+    if (c0 + 256 <= padded) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c0 + lane + 32 * e;
-      if (c < padded) out[c] = static_cast<int8_t>(k[e]);
+      for (int e = 0; e < 8; ++e) p[32 * e] = static_cast<int8_t>(k[e]);
+    } else {
+      const int n = padded - c0 - lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (32 * e < n) p[32 * e] = static_cast<int8_t>(k[e]);
     }
   }
 }
@@ -167,7 +173,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf, int warp,
 }
 
 // Three blocks of 16 warps per SM where rows take four steps: 300 rows of 11003
-// need no second wave (10.1 -> 7.0 us).
+// need no second wave (10.1 -> 7.0 us, 5.1 with accesses at fixed distances).
 template <typename T, int G, int VEC>
 __global__ void __launch_bounds__(G == 1 ? 1024 : 512, G == 1 || sizeof(T) == 4 ? 2 : 3)
     quantize_rows_kernel(const QuantArgs a) {

@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 namespace qlora {
 
@@ -203,46 +204,58 @@ __device__ __forceinline__ Raw8<T> raw_ones() {
 
 // The lane's eight columns of row[c0 ..] (global or shared memory), zeros past
 // the end.
-template <int VEC, typename T>
+template <int VEC, bool SPLIT = true, typename T>
 __device__ __forceinline__ Raw8<T> load_cols(const T* row, int c0, int cols, int lane) {
   if constexpr (VEC) {
     const int c = c0 + lane * 8;
     return VEC == kWhole || c < cols ? load_group(row + c) : raw_zero<T>();
-  } else if constexpr (sizeof(T) == 4) {
-    Raw8<T> r;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c0 + lane + 32 * e;
-      r.w[e] = c < cols ? reinterpret_cast<const uint32_t*>(row)[c] : 0u;
-    }
-    return r;
   } else {
-    Raw8<T> r;
+    // No column is past the end but in a row's last step: unconditional
+    // accesses at fixed distances otherwise (layer norm of 4096 x 4095 in bf16
+    // 41.2 -> 24.2 us).  SPLIT = false takes one path for both.
+    using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+    const Bits* p = reinterpret_cast<const Bits*>(row) + (c0 + lane);
     uint32_t h[8];
+    if (SPLIT && c0 + 256 <= cols) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c0 + lane + 32 * e;
-      h[e] = c < cols ? reinterpret_cast<const uint16_t*>(row)[c] : 0u;
+      for (int e = 0; e < 8; ++e) h[e] = p[32 * e];
+    } else {
+      const int n = cols - c0 - lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = 32 * e < n ? p[32 * e] : 0u;
     }
+    Raw8<T> r;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) r.w[p] = h[2 * p] | (h[2 * p + 1] << 16);
+      for (int e = 0; e < 8; ++e) r.w[e] = h[e];
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r.w[q] = __byte_perm(h[2 * q], h[2 * q + 1], 0x5410);
+    }
     return r;
   }
 }
 
-template <int VEC, typename T>
+template <int VEC, bool SPLIT = true, typename T>
 __device__ __forceinline__ void store_cols(T* row, int c0, int cols, int lane, const Raw8<T>& r) {
   if constexpr (VEC) {
     const int c = c0 + lane * 8;
     if (VEC == kWhole || c < cols) store_group(row + c, r);
   } else {
+    using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+    Bits* p = reinterpret_cast<Bits*>(row) + (c0 + lane);
+    const auto bits = [&](int e) {
+      return sizeof(T) == 4 ? static_cast<Bits>(r.w[e % (sizeof(T) * 2)])
+                            : static_cast<Bits>(r.w[e >> 1] >> (16 * (e & 1)));
+    };
+    if (SPLIT && c0 + 256 <= cols) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c0 + lane + 32 * e;
-      if (c < cols) {
-        if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(row)[c] = r.w[e];
-        else reinterpret_cast<uint16_t*>(row)[c] = static_cast<uint16_t>(r.w[e >> 1] >> (16 * (e & 1)));
-      }
+      for (int e = 0; e < 8; ++e) p[32 * e] = bits(e);
+    } else {
+      const int n = cols - c0 - lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (32 * e < n) p[32 * e] = bits(e);
     }
   }
 }
@@ -299,9 +312,9 @@ struct KeepGroup {  // of one group, straight from its draws
     return ((e & 1) ? r.w[e >> 1] : (r.w[e >> 1] << 16)) > above || all;
   }
 };
-struct KeepBits {  // bit e: element e
+struct KeepBits {  // bit 4 e: element e
   uint32_t bits;
-  __device__ __forceinline__ bool operator()(int e) const { return (bits >> e) & 1u; }
+  __device__ __forceinline__ bool operator()(int e) const { return (bits >> (4 * e)) & 1u; }
 };
 
 __device__ __forceinline__ KeepGroup keep_group(const DropArgs& d, uint64_t counter) {
@@ -316,13 +329,13 @@ __device__ __forceinline__ auto keep_cols(const DropArgs& d, uint64_t counter0, 
   if constexpr (VEC) {
     return own;
   } else {
-    uint32_t bits = 0, m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) bits |= (own(e) ? 1u : 0u) << e;
+    // Column lane + 32 e is element lane % 8 of the group of lane (lane / 8 + 4 e):
+    // of the eight ballots a lane needs the one of its element.
+    uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int col = lane + 32 * e;
-      m |= ((__shfl_sync(0xFFFFFFFFu, bits, col >> 3) >> (col & 7)) & 1u) << e;
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, own(e));
+      if ((lane & 7) == e) m = all >> (lane >> 3);
     }
     return KeepBits{m};
   }
