@@ -143,6 +143,8 @@ qlora_status qlora_dropout_fwd(const void* X, const void* residual, void* Y, int
   if (!aligned_to(X, es) || !aligned_to(Y, es) || !aligned_to(residual, es) ||
       !make_drop_args(p, seed, offset, offset_dev, cols, &d))
     return QLORA_ERR_ALIGNMENT;
+  const int64_t n = rows * cols * es;
+  if (!disjoint({{Y, n}}, {{X, n}, {residual, n}})) return QLORA_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(st, "dropout", 1);
   const cudaError_t e = launch_dropout(dtype, X, residual, Y, rows, cols, d, st);

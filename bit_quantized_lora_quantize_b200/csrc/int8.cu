@@ -821,6 +821,9 @@ cudaError_t launch_matmul_int8(int32_t dtype, const int8_t* xq, int64_t ldx, con
 }
 
 // Row strides in bytes: multiples of 16 that hold a row, below TMA's 2^40.
+int64_t code_bytes(int64_t rows, int64_t ld, int64_t used) {  // from the first row to the end of the last
+  return rows - 1 > (int64_t(1) << 61) / ld ? int64_t(1) << 61 : (rows - 1) * ld + used;
+}
 bool bad_stride(int64_t ld, int64_t K) { return ld < K || ld % 16 != 0 || ld >= (int64_t(1) << 40); }
 
 }  // namespace
@@ -838,6 +841,9 @@ qlora_status qlora_quantize_int8(const void* X, int64_t rows, int64_t cols, int3
   if (sh != QLORA_OK) return sh;
   if (bad_stride(ld, cols)) return QLORA_ERR_INVALID_ARG;
   if (!aligned_to(X, dtype_bytes(dtype)) || !aligned16(codes) || !aligned_to(scale, 4)) return QLORA_ERR_ALIGNMENT;
+  if (!disjoint({{codes, code_bytes(rows, ld, padded_depth(cols))}, {scale, rows * 4}},
+                {{X, rows * cols * dtype_bytes(dtype)}}))
+    return QLORA_ERR_INVALID_ARG;
   const QuantArgs a{X, codes, scale, rows, ld, static_cast<int>(cols), 1};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(st, "quantize_int8", 1);
@@ -862,6 +868,9 @@ qlora_status qlora_matmul_int8(const int8_t* Xq, int64_t ldx, const float* x_sca
     return QLORA_ERR_ALIGNMENT;
   if (!workspace || ws_bytes < int8_layout(M, K, N).total) return QLORA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
+  if (!disjoint({{Y, M * N * dtype_bytes(dtype)}}, {{Xq, code_bytes(M, ldx, K)}, {Wq, code_bytes(N, ldw, K)},
+                                                   {x_scale, M * 4}, {w_scale, N * 4}}))
+    return QLORA_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(st, "matmul_int8", 1);
   const cudaError_t e = launch_matmul_int8(dtype, Xq, ldx, x_scale, M, K, N, Wq, ldw, w_scale, Y,
@@ -883,6 +892,8 @@ qlora_status qlora_linear_int8_fwd(const void* X, int64_t M, int64_t K, int64_t 
   const Int8Layout l = int8_layout(M, K, N);
   if (!workspace || ws_bytes < l.total) return QLORA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
+  if (!disjoint({{Y, M * N * es}}, {{X, M * K * es}, {Wq, code_bytes(N, ldw, K)}, {w_scale, N * 4}}))
+    return QLORA_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int8_t* codes = reinterpret_cast<int8_t*>(ws + l.codes);
   float* scale = reinterpret_cast<float*>(ws + l.scale);

@@ -965,6 +965,10 @@ qlora_status fwd_call(LnFwdArgs& a, const DropArgs* drop, int64_t rows, int64_t 
   if (!aligned_to(a.x, es) || !aligned_to(a.y, es) || !aligned_to(a.residual, es) || !aligned_to(a.z, es) ||
       !aligned_to(a.w, ws) || !aligned_to(a.b, ws) || !aligned_to(a.mean, 4) || !aligned_to(a.rstd, 4))
     return QLORA_ERR_ALIGNMENT;
+  const int64_t n = rows * cols * es;
+  if (!disjoint({{a.y, n}, {a.z, n}, {a.mean, rows * 4}, {a.rstd, rows * 4}},
+                {{a.x, n}, {a.residual, n}, {a.w, cols * ws}, {a.b, cols * ws}}))
+    return QLORA_ERR_INVALID_ARG;
   a.rows = rows;
   a.cols = static_cast<int>(cols);
   a.eps = eps;
@@ -988,6 +992,11 @@ qlora_status bwd_call(LnBwdArgs& a, int64_t rows, int64_t cols, int32_t dtype, i
     return QLORA_ERR_ALIGNMENT;
   if (!workspace || ws_bytes < ln_workspace_bytes(cols)) return QLORA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
+  const int64_t n = rows * cols * es;
+  if (!disjoint({{a.dx, n}, {a.dres, n}, {dweight, cols * 4}, {dbias, cols * 4}},
+                {{a.dy, n}, {a.dz, n}, {a.z, n}, {a.mean, rows * 4}, {a.rstd, rows * 4},
+                 {a.w, cols * dtype_bytes(wdtype)}}))
+    return QLORA_ERR_INVALID_ARG;
   a.rows = rows;
   a.cols = static_cast<int>(cols);
   a.inv_n = static_cast<float>(1.0 / static_cast<double>(cols));

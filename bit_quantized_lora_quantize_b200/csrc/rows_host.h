@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 #include "../../include/qlora.h"
 #include "rows_device.cuh"
@@ -23,6 +24,26 @@ inline bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uint
 inline int aligned_layout(int64_t cols) { return cols % 256 == 0 ? kWhole : kAligned; }
 // Rows of whole 16-byte vectors: eight-element groups never straddle rows.
 inline bool vector_rows(const void* p, int64_t cols) { return cols % 8 == 0 && aligned_to(p, 16); }
+
+// Memory a call reads or writes; none where the pointer is null.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+// The outputs share no byte with an input or with one another.
+inline bool disjoint(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  const auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && (x < y ? y - x < static_cast<uintptr_t>(a.bytes) : x - y < static_cast<uintptr_t>(b.bytes));
+  };
+  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span& i : inputs)
+      if (meet(*o, i)) return false;
+    for (const Span* other = outputs.begin(); other != o; ++other)
+      if (meet(*o, *other)) return false;
+  }
+  return true;
+}
 
 inline qlora_status check_rows(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0) return QLORA_ERR_INVALID_ARG;

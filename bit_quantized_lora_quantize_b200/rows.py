@@ -4,6 +4,7 @@ and the linear whose adapter sees dropped inputs (formulas in include/qlora.h).
 
 A tensor of any shape is a matrix whose rows run along its last dimension.
 Every call runs on the tensors' device, on that device's current stream.
+Outputs passed in share no memory with the inputs or with one another.
 """
 
 from __future__ import annotations

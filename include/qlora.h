@@ -290,9 +290,9 @@ QLORA_API qlora_status qlora_silu_gate_bwd(const uint16_t* G, const uint16_t* U,
  * pointers need the alignment of their elements only (rows of whole 16-byte
  * vectors take wider accesses).  Arithmetic is float32 with one rounding per
  * output.  rows and cols are at least 1, rows below 2^31, cols below
- * 2^31 - 2^16, rows * cols at most 2^40 (QLORA_ERR_UNSUPPORTED).  Outputs may
- * not alias inputs.  Glue between
- * LoRA linears, like the SiLU gate: the pages have no counterpart.
+ * 2^31 - 2^16, rows * cols at most 2^40 (QLORA_ERR_UNSUPPORTED).  Outputs
+ * share no memory with an input or with one another (QLORA_ERR_INVALID_ARG).
+ * Glue between LoRA linears, like the SiLU gate: the pages have no counterpart.
  */
 typedef enum { QLORA_DTYPE_BF16 = 0, QLORA_DTYPE_FP16 = 1, QLORA_DTYPE_FP32 = 2 } qlora_dtype;
 
@@ -413,7 +413,9 @@ QLORA_API size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols);
  * `ld` bytes apart: a multiple of 16 that holds a row (QLORA_ERR_INVALID_ARG);
  * quantization fills a row up to the next multiple of 16 columns with zeros,
  * and the product does not read past K.  codes are 16-byte aligned, X and Y as
- * their elements.
+ * their elements.  Outputs share no memory with an input or with one another
+ * (QLORA_ERR_INVALID_ARG; rows of codes count from the first to the end of the
+ * last).
  * qlora_linear_int8_fwd quantizes X into the workspace and multiplies.
  * M, K, N >= 1, K <= 133144 (sums stay exact in 32 bits), M, N < 2^31 - 2^15;
  * otherwise QLORA_ERR_UNSUPPORTED.  Results do not depend on the order of

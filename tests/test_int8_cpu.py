@@ -59,3 +59,23 @@ def test_binding_refuses_cpu_tensors():
                  lambda: q.qlora_matmul_int8(w, w)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_overlapping_tensors_are_refused(L):
+    """Rows of codes count from the first row to the end of the last."""
+    X, C, S = FAKE, FAKE + 65536, FAKE + 2 * 65536
+
+    def quant(codes=C, scale=S, ld=32):
+        return L.qlora_quantize_int8(X, 4, 30, BF16, codes, ld, scale, None)
+    assert quant(codes=X) == 1 and quant(codes=X + 224) == 1 and quant(scale=X + 236) == 1
+    assert quant(scale=C + 124) == 1 and quant(codes=X - 96) == 1 and quant(codes=X - 320, ld=112) == 1
+    need = L.qlora_int8_workspace_bytes(4, 30, 8)
+    ws = FAKE + 3 * 65536
+
+    def mm(y, w=C):
+        return L.qlora_matmul_int8(X, 32, S, 4, 30, 8, w, 32, S + 4096, y, BF16, ws, need, None)
+    assert mm(X + 124) == 1 and mm(C + 252) == 1 and mm(S - 62) == 1 and mm(S + 4096 + 30) == 1
+
+    def lin(y):
+        return L.qlora_linear_int8_fwd(X, 4, 30, 8, BF16, C, 32, S, y, ws, need, None)
+    assert lin(X) == 1 and lin(X + 238) == 1 and lin(C + 252) == 1 and lin(S + 30) == 1 and lin(X - 62) == 1

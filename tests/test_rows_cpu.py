@@ -104,3 +104,34 @@ def test_binding_refuses_cpu_tensors():
                  lambda: q.qlora_dropout_add_layernorm_fwd(x, x, 0.1, 1)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_overlapping_tensors_are_refused(L):
+    """4 rows of 8 bf16 values take 64 bytes: an output may begin where an
+    input ends, not before."""
+    X, Y, Z, R = (FAKE + i * 4096 for i in range(4))
+
+    def drop(y, res=None, rows=4):
+        return L.qlora_dropout_fwd(X, res, y, rows, 8, BF16, 0.1, 1, 2, None, None)
+    assert drop(X) == 1 and drop(X + 62) == 1 and drop(X - 62) == 1 and drop(R + 2, res=R) == 1
+    assert L.qlora_dropout_bwd(X, X, 4, 8, BF16, 0.1, 1, 2, None, None) == 1
+
+    def norm(y=Y, m=Z, r=R, w=None):
+        return L.qlora_layernorm_fwd(X, w, None, y, m, r, 4, 8, BF16, FP32, ctypes.c_float(1e-5), None)
+    assert norm(y=X) == 1 and norm(m=X + 60) == 1 and norm(r=Z + 12) == 1 and norm(w=Y + 60) == 1
+
+    def norm_bwd(dx=Y, dw=Z, db=R):
+        return L.qlora_layernorm_bwd(X, X + 4096 * 8, X + 4096 * 9, X + 4096 * 10, None, dx, dw, db, 4, 8, BF16, BF16,
+                                     X + 4096 * 11, WS, None)
+    assert norm_bwd(dx=X) == 1 and norm_bwd(dx=X + 4096 * 8 + 32) == 1
+    assert norm_bwd(db=Z) == 1 and norm_bwd(dw=Y + 60) == 1 and norm_bwd(dw=X + 4096 * 9 + 12) == 1
+
+    def fused(z=Z, y=Y, res=R):
+        return L.qlora_dropout_add_layernorm_fwd(X, res, None, None, z, y, None, None, 4, 8, BF16, BF16,
+                                                 ctypes.c_float(1e-5), 0.1, 1, 2, None, None)
+    assert fused(z=Y) == 1 and fused(z=R) == 1 and fused(y=X) == 1 and fused(res=Z + 62) == 1
+
+    def fused_bwd(dx=Z, dres=R, dz=None):
+        return L.qlora_dropout_add_layernorm_bwd(X, dz, Y, X + 4096 * 9, X + 4096 * 10, None, dx, dres, None, None, 4, 8,
+                                                 BF16, BF16, 0.1, 1, 2, None, X + 4096 * 11, WS, None)
+    assert fused_bwd(dx=R) == 1 and fused_bwd(dx=X) == 1 and fused_bwd(dres=Y + 2) == 1 and fused_bwd(dz=Z) == 1
