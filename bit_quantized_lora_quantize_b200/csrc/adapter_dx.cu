@@ -75,7 +75,15 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int rows_k = static_cast<int>(min(static_cast<int64_t>(kTileK), K - k0));
   const uint16_t* u_src = U + (m0 + crow) * 2 * rp + chunk * 8;
   const uint16_t* a_src = A + (k0 + crow) * r + chunk * 8;
-  const auto fetch = [&](int j0) {
+  const auto fetch_a = [&](int j0) {
+#pragma unroll
+    for (int t = 0; t < kTileK / 32; ++t) {
+      const int row = crow + t * 32;
+      const bool in = row < rows_k && j0 + chunk * 8 < r;
+      copy16(s_a + a_offset(row, chunk), in ? a_src + t * 32 * r + j0 : A, in);
+    }
+  };
+  const auto fetch_u = [&](int j0) {
 #pragma unroll
     for (int t = 0; t < kTileM / 32; ++t) {
       const int row = crow + t * 32;
@@ -84,15 +92,12 @@ __global__ void __launch_bounds__(kThreads, 3)
       copy16(s_hi + u_offset(row, chunk), p, in);
       copy16(s_lo + u_offset(row, chunk), p + (in ? rp : 0), in);
     }
-#pragma unroll
-    for (int t = 0; t < kTileK / 32; ++t) {
-      const int row = crow + t * 32;
-      const bool in = row < rows_k && j0 + chunk * 8 < r;
-      copy16(s_a + a_offset(row, chunk), in ? a_src + t * 32 * r + j0 : A, in);
-    }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch(0);
+  // A is ready before the GEMM that computes U and the rest of dX starts.
+  fetch_a(0);
+  griddep_wait();
+  fetch_u(0);
 
   float acc[2][4][4];
 #pragma unroll
@@ -105,7 +110,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   for (int j0 = 0; j0 < rp; j0 += kRanks) {
     if (j0) {
       __syncthreads();  // the previous step's fragments have been read
-      fetch(j0);
+      fetch_a(j0);
+      fetch_u(j0);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
@@ -183,9 +189,15 @@ cudaError_t launch_adapter_dx(const uint16_t* Upair, const uint16_t* A, uint16_t
     part.offset += static_cast<uint64_t>(m0) * d.groups;
     const dim3 grid(static_cast<unsigned>((K + kTileK - 1) / kTileK),
                     static_cast<unsigned>(row_blocks - b < kMaxRowBlocks ? row_blocks - b : kMaxRowBlocks));
-    adapter_dx_kernel<<<grid, kThreads, 0, stream>>>(Upair + m0 * 2 * lora_pad(r), A, dX + m0 * K, M - m0, K, r,
-                                                     lora_pad(r), part);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = pdl_attribute();
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, adapter_dx_kernel, Upair + m0 * 2 * lora_pad(r), A, dX + m0 * K,
+                                             M - m0, K, r, lora_pad(r), part);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -19,6 +19,7 @@
 
 #include "abi_internal.h"
 #include "kernels.h"
+#include "ptx.cuh"
 #include "rows_host.h"
 
 namespace qlora {
@@ -36,6 +37,7 @@ template <typename T, bool RES, int U>
 __global__ void __launch_bounds__(kDropThreads)
     dropout_vec_kernel(const T* __restrict__ X, const T* __restrict__ R, T* __restrict__ Y, int64_t ngroups,
                        const DropArgs d) {
+  griddep_launch_dependents();  // a GEMM that reads Y may set itself up meanwhile
   const int64_t g0 = static_cast<int64_t>(blockIdx.x) * (kDropThreads * U) + threadIdx.x;
   const uint64_t base = drop_base(d);
   Raw8<T> x[U], r[U];

@@ -109,12 +109,11 @@ struct NoDrop {};
 template <bool FUSED>
 using FwdDrop = std::conditional_t<FUSED, DropArgs, NoDrop>;
 
-
 // Values of one lane's eight columns after the residual dropout, rounded to
 // T and stored to Z.
 template <typename T, int VEC>
-__device__ __forceinline__ Raw8<T> add_dropped(const LnFwdArgs& a, const DropArgs& drop, int64_t row, int c0, int lane, uint64_t base,
-                                               const Raw8<T>& x, const Raw8<T>& r) {
+__device__ __forceinline__ Raw8<T> add_dropped(const LnFwdArgs& a, const DropArgs& drop, int64_t row, int c0, int lane,
+                                               uint64_t base, const Raw8<T>& x, const Raw8<T>& r) {
   const auto keep = keep_cols<VEC>(drop, base + row * drop.groups + c0 / 8, lane);
   float v[8];
 #pragma unroll
@@ -167,7 +166,8 @@ __device__ __forceinline__ void normalise(const LnFwdArgs& a, int64_t row, int c
 }
 
 template <typename T, typename W, int G, int VEC, bool FUSED>
-__global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1)) ln_fwd_kernel(const LnFwdArgs a, const FwdDrop<FUSED> drop) {
+__global__ void __launch_bounds__(kFwdWarps * 32 * (G == 1 ? 2 : 1))
+    ln_fwd_kernel(const LnFwdArgs a, const FwdDrop<FUSED> drop) {
   __shared__ float red[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = warp & (a.wpr - 1), first = warp - part, shift = __ffs(a.wpr) - 1;
