@@ -13,8 +13,8 @@
 //   30.6 us);
 // - up to 16 tokens, bound by reading the weight: `token_kernel` streams it
 //   straight into the register fragments of mma.sync (one token, 8192 x 8192:
-//   15.5 us of which 10.3 are the weight at the copy bandwidth; 22016 x 8192:
-//   35.4 us, 0.78 of it);
+//   15.6 us of which 10.3 are the weight at the copy bandwidth; four tokens,
+//   22016 x 8192: 34.9 us, 0.79 of it);
 // - more tokens: `pair_kernel`, CTA pairs (cta_group::2) with 256 x 256 tiles
 //   fed by a TMA ring; persistent, with two accumulators in TMEM so that a
 //   tile's epilogue runs under the next tile's products (4096 x 8192 x 8192:
@@ -265,8 +265,9 @@ cudaError_t launch_quantize_int8(int32_t dtype, const QuantArgs& a, cudaStream_t
 // eight rows together; each group's partial sums meet in shared memory.
 constexpr int kTokenMax = 16;
 constexpr int kTokenWarps = 16;
-constexpr int kTokenBatch = 8;   // 64-deep steps in flight per warp, twice
+constexpr int kTokenBatch = 4;   // 64-deep steps of two row groups in flight per warp, twice
 constexpr int kTokenSlots = 4;   // row groups between two exchanges
+static_assert(kTokenSlots % 2 == 0, "pairs of groups");
 
 struct TokenArgs {
   const int8_t* x;
@@ -328,52 +329,71 @@ __global__ void __launch_bounds__(kTokenWarps * 32, 1) token_kernel(const TokenA
   const int8_t* x0 = a.x + static_cast<int64_t>(min(g, a.M - 1)) * a.ldx;
   const int8_t* x1 = a.x + static_cast<int64_t>(min(g + 8, a.M - 1)) * a.ldx;
 
-  uint4 next[kTokenBatch];
+  uint4 next[2][kTokenBatch] = {};
   const auto fetch = [&](int group, int batch) {
     const int s = s0 + batch * kTokenBatch;
-    const int8_t* p = row_of(group) + s * 64 + q * 16;
 #pragma unroll
-    for (int i = 0; i < kTokenBatch; ++i)
-      if (s + i < s1) next[i] = load_stream(p + i * 64);
+    for (int h = 0; h < 2; ++h) {
+      if (group + h < g1) {
+        const int8_t* p = row_of(group + h) + s * 64 + q * 16;
+#pragma unroll
+        for (int i = 0; i < kTokenBatch; ++i)
+          if (s + i < s1) next[h][i] = load_stream(p + i * 64);
+      }
+    }
   };
   // The weight is ready before the kernel that quantizes the tokens started.
   if (!a.chained) griddep_wait();
   if (g0 < g1) fetch(g0, 0);
   if (a.chained) griddep_wait();
 
-  int c[4] = {0, 0, 0, 0};
+  int c[2][4] = {};
   for (int from = g0; from < g1; from += kTokenSlots) {
     const int to = min(g1, from + kTokenSlots);
-    for (int group = from; group < to; ++group) {
+    // Two groups at a time share the tokens' fragments (one token, 4096 x 4096:
+    // 6.8 -> 5.5 us; 16 tokens, 11008 x 4096: 19.2 -> 15.9).
+    for (int group = from; group < to; group += 2) {
+      const bool pair = group + 1 < to;
       for (int batch = 0; batch < batches; ++batch) {
-        uint4 w[kTokenBatch];
+        uint4 w[2][kTokenBatch];
 #pragma unroll
-        for (int i = 0; i < kTokenBatch; ++i) w[i] = next[i];
+        for (int i = 0; i < kTokenBatch; ++i) {
+          w[0][i] = next[0][i];
+          w[1][i] = next[1][i];
+        }
         if (batch + 1 < batches) fetch(group, batch + 1);
-        else if (group + 1 < g1) fetch(group + 1, 0);
+        else if (group + 2 < g1) fetch(group + 2, 0);
         const int s = s0 + batch * kTokenBatch, at = s * 64 + q * 16;
 #pragma unroll
         for (int i = 0; i < kTokenBatch; ++i) {
           if (s + i < s1) {
             const uint4 x = *reinterpret_cast<const uint4*>(x0 + at + i * 64);
             const uint4 z = TWO ? *reinterpret_cast<const uint4*>(x1 + at + i * 64) : make_uint4(0, 0, 0, 0);
-            mma_s8(c, x.x, z.x, x.y, z.y, w[i].x, w[i].y);
-            mma_s8(c, x.z, z.z, x.w, z.w, w[i].z, w[i].w);
+            mma_s8(c[0], x.x, z.x, x.y, z.y, w[0][i].x, w[0][i].y);
+            mma_s8(c[0], x.z, z.z, x.w, z.w, w[0][i].z, w[0][i].w);
+            if (pair) {
+              mma_s8(c[1], x.x, z.x, x.y, z.y, w[1][i].x, w[1][i].y);
+              mma_s8(c[1], x.z, z.z, x.w, z.w, w[1][i].z, w[1][i].w);
+            }
           }
         }
       }
-      if (tail) {
-        const int at = steps * 64 + q * 16;
-        const uint4 w = load_tail(row_of(group), at, a.K), x = load_tail(x0, at, a.K);
-        const uint4 z = TWO ? load_tail(x1, at, a.K) : make_uint4(0, 0, 0, 0);
-        mma_s8(c, x.x, z.x, x.y, z.y, w.x, w.y);
-        mma_s8(c, x.z, z.z, x.w, z.w, w.z, w.w);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !pair) break;
+        if (tail) {
+          const int at = steps * 64 + q * 16;
+          const uint4 w = load_tail(row_of(group + h), at, a.K), x = load_tail(x0, at, a.K);
+          const uint4 z = TWO ? load_tail(x1, at, a.K) : make_uint4(0, 0, 0, 0);
+          mma_s8(c[h], x.x, z.x, x.y, z.y, w.x, w.y);
+          mma_s8(c[h], x.z, z.z, x.w, z.w, w.z, w.w);
+        }
+        // c[h][0], c[h][1]: token g, rows 2 q and 2 q + 1 of the group; c[h][2], c[h][3]: token g + 8
+        int* out = sums[group + h - from][warp];
+        *reinterpret_cast<int2*>(out + g * 8 + 2 * q) = make_int2(c[h][0], c[h][1]);
+        if (TWO) *reinterpret_cast<int2*>(out + (g + 8) * 8 + 2 * q) = make_int2(c[h][2], c[h][3]);
+        c[h][0] = c[h][1] = c[h][2] = c[h][3] = 0;
       }
-      // c[0], c[1]: token g, rows 2 q and 2 q + 1 of the group; c[2], c[3]: token g + 8
-      int* out = sums[group - from][warp];
-      *reinterpret_cast<int2*>(out + g * 8 + 2 * q) = make_int2(c[0], c[1]);
-      if (TWO) *reinterpret_cast<int2*>(out + (g + 8) * 8 + 2 * q) = make_int2(c[2], c[3]);
-      c[0] = c[1] = c[2] = c[3] = 0;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < (to - from) * 8 * a.M; i += kTokenWarps * 32) {
