@@ -218,7 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_acc = *tmem_slot;
   int unit = static_cast<int>(blockIdx.x >> 1);
-  if (args.ctr) unit = rank == 0 ? *unit_slot : ld_cluster_s32(map_rank(unit_slot, 0));
+  if (args.ctr) {
+    unit = rank == 0 ? *unit_slot : ld_cluster_s32(map_rank(unit_slot, 0));
+    // Tickets past the last come only from a second call that runs on the same
+    // workspace: its results are lost, but it stays inside its tensors.
+    unit = min(unit, args.units - 1);
+  }
   // Ticket order: rank units; tiles [0, early); tail units [0, t_first);
   // the other tiles; the other tail units.
   const bool runit = unit < args.r_units;
