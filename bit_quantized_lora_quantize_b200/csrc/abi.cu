@@ -283,8 +283,7 @@ qlora_status linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, cons
     // back through a padded buffer.
     uint16_t* Ap = reinterpret_cast<uint16_t*>(ws + wl.pa_off);
     uint16_t* Bp = reinterpret_cast<uint16_t*>(ws + wl.pb_off);
-    cudaError_t e = launch_pad_copy(A, K, r, r, Ap, r8, r8, 2, st);
-    if (e == cudaSuccess) e = launch_pad_copy(B, r, N, N, Bp, N, N, 2, st, r8);
+    const cudaError_t e = launch_pad_copies({{A, K, r, Ap, K, r8, 2}, {B, r, N, Bp, r8, N, 2}}, st);
     if (e != cudaSuccess) return cuda_fail(e);
     Ak = Ap;
     Bk = Bp;
@@ -323,7 +322,7 @@ qlora_status linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, cons
                          reinterpret_cast<int*>(ws + wl.cf_off));
     p2.done();
   }
-  if (e == cudaSuccess && r8 != r) e = launch_pad_copy(Tk, M, r8, r8, T_save, r, r, 4, st);
+  if (e == cudaSuccess && r8 != r) e = launch_pad_copies({{Tk, M, r8, T_save, M, r, 4}}, st);
   return e == cudaSuccess ? QLORA_OK : cuda_fail(e);
 }
 
@@ -366,9 +365,7 @@ qlora_status linear_bwd(const uint16_t* dY, const uint16_t* X, const float* T_sa
     uint16_t* Ap = reinterpret_cast<uint16_t*>(ws + wl.pa_off);
     uint16_t* Bp = reinterpret_cast<uint16_t*>(ws + wl.pb_off);
     float* Tp = reinterpret_cast<float*>(ws + wl.pt_off);
-    e = launch_pad_copy(A, K, r, r, Ap, r8, r8, 2, st);
-    if (e == cudaSuccess) e = launch_pad_copy(B, r, N, N, Bp, N, N, 2, st, r8);
-    if (e == cudaSuccess) e = launch_pad_copy(T_save, M, r, r, Tp, r8, r8, 4, st);
+    e = launch_pad_copies({{A, K, r, Ap, K, r8, 2}, {B, r, N, Bp, r8, N, 2}, {T_save, M, r, Tp, M, r8, 4}}, st);
     if (e != cudaSuccess) return cuda_fail(e);
     Ak = Ap;
     Bk = Bp;
@@ -401,10 +398,7 @@ qlora_status linear_bwd(const uint16_t* dY, const uint16_t* X, const float* T_sa
     e = launch_adapter_dx(Upair, Ak, dX, M, K, r8, *drop, st);
     p3.done();
   }
-  if (e == cudaSuccess && r8 != r) {
-    e = launch_pad_copy(dAk, K, r8, r8, dA, r, r, 4, st);
-    if (e == cudaSuccess) e = launch_pad_copy(dBk, r, N, N, dB, N, N, 4, st);
-  }
+  if (e == cudaSuccess && r8 != r) e = launch_pad_copies({{dAk, K, r8, dA, K, r, 4}, {dBk, r8, N, dB, r, N, 4}}, st);
   return e == cudaSuccess ? QLORA_OK : cuda_fail(e);
 }
 

@@ -93,33 +93,41 @@ int glue_grid(int64_t n8) {
   return static_cast<int>(std::max<int64_t>(1, std::min(want, cap)));
 }
 
+struct PadCopies {
+  PadCopy job[kMaxPadCopies];
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kGlueThreads) pad_copy_kernel(const T* __restrict__ src, int64_t rows,
-                                                                int64_t src_cols, int64_t src_ld, T* __restrict__ dst,
-                                                                int64_t dst_cols, int64_t dst_ld, int64_t dst_rows) {
-  const int64_t n = dst_rows * dst_cols;
+__device__ __forceinline__ void pad_copy(const PadCopy& j) {
+  const T* src = static_cast<const T*>(j.src);
+  T* dst = static_cast<T*>(j.dst);
+  const int64_t n = j.dst_rows * j.dst_cols;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
-    const int64_t r = i / dst_cols, c = i - r * dst_cols;
-    dst[r * dst_ld + c] = (r < rows && c < src_cols) ? src[r * src_ld + c] : T(0);
+    const int64_t r = n >> 32 ? i / j.dst_cols : static_cast<uint32_t>(i) / static_cast<uint32_t>(j.dst_cols);
+    const int64_t c = i - r * j.dst_cols;
+    dst[r * j.dst_cols + c] = (r < j.rows && c < j.src_cols) ? src[r * j.src_cols + c] : T(0);
   }
+}
+
+// One matrix per row of blocks.
+__global__ void __launch_bounds__(kGlueThreads) pad_copy_kernel(const __grid_constant__ PadCopies jobs) {
+  const PadCopy& j = jobs.job[blockIdx.y];
+  if (j.elem_bytes == 2) pad_copy<uint16_t>(j);
+  else pad_copy<uint32_t>(j);
 }
 
 }  // namespace
 
-cudaError_t launch_pad_copy(const void* src, int64_t rows, int64_t src_cols, int64_t src_ld, void* dst,
-                            int64_t dst_cols, int64_t dst_ld, int elem_bytes, cudaStream_t stream,
-                            int64_t dst_rows) {
-  if (dst_rows < 0) dst_rows = rows;
-  const int grid = glue_grid((dst_rows * dst_cols + 7) / 8);
-  if (elem_bytes == 2)
-    pad_copy_kernel<uint16_t><<<grid, kGlueThreads, 0, stream>>>(static_cast<const uint16_t*>(src), rows, src_cols,
-                                                                  src_ld, static_cast<uint16_t*>(dst), dst_cols,
-                                                                  dst_ld, dst_rows);
-  else
-    pad_copy_kernel<uint32_t><<<grid, kGlueThreads, 0, stream>>>(static_cast<const uint32_t*>(src), rows, src_cols,
-                                                                  src_ld, static_cast<uint32_t*>(dst), dst_cols,
-                                                                  dst_ld, dst_rows);
+cudaError_t launch_pad_copies(std::initializer_list<PadCopy> copies, cudaStream_t stream) {
+  PadCopies jobs{};
+  unsigned count = 0;
+  int64_t most = 0;
+  for (const PadCopy& j : copies) {
+    most = std::max(most, j.dst_rows * j.dst_cols);
+    jobs.job[count++] = j;
+  }
+  pad_copy_kernel<<<dim3(glue_grid(most), count, 1), kGlueThreads, 0, stream>>>(jobs);
   return cudaGetLastError();
 }
 

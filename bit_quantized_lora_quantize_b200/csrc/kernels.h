@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 #include "nf4_device.cuh"
 
@@ -117,13 +118,18 @@ cudaError_t launch_small_m_rd(const uint16_t* X, const uint8_t* codes, const uin
                               int64_t N, int r, float scale, uint16_t* Y, float* T_save, void* scratch, int* status,
                               const Nf4Params& P, cudaStream_t stream);
 
-// Copy a rows x src_cols matrix (row stride src_ld elements of elem_bytes,
-// 2 or 4) into dst (row stride dst_ld), filling columns [src_cols, dst_cols)
-// and rows [rows, dst_rows) with zeros (dst_rows = rows when omitted).  Used to
-// pad the adapter and its gradients to a multiple of 8 ranks.
-cudaError_t launch_pad_copy(const void* src, int64_t rows, int64_t src_cols, int64_t src_ld, void* dst,
-                            int64_t dst_cols, int64_t dst_ld, int elem_bytes, cudaStream_t stream,
-                            int64_t dst_rows = -1);
+// Row-major copies into matrices of other sizes, zeros outside the source, all
+// in one launch (at most kMaxPadCopies).  They pad the adapter to a rank that
+// is a multiple of eight and take its results back.
+struct PadCopy {
+  const void* src;  // [rows x src_cols]
+  int64_t rows, src_cols;
+  void* dst;        // [dst_rows x dst_cols]
+  int64_t dst_rows, dst_cols;
+  int elem_bytes;   // 2 or 4
+};
+constexpr int kMaxPadCopies = 3;
+cudaError_t launch_pad_copies(std::initializer_list<PadCopy> copies, cudaStream_t stream);
 
 // SiLU gate of a gated MLP (glue between linears): H = silu(G) * U and its
 // backward dG, dU, elementwise over n bf16 values.
