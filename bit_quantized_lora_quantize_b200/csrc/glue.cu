@@ -110,7 +110,9 @@ __device__ __forceinline__ void pad_copy(const PadCopy& j) {
   }
 }
 
-// One matrix per row of blocks.
+// One matrix per row of blocks, one element per thread and step: bound by the
+// latency of a launch, so one launch serves several matrices (forward and
+// backward of 300 x 1024 x 2000 at rank 33: 85 us with one launch each, 62).
 __global__ void __launch_bounds__(kGlueThreads) pad_copy_kernel(const __grid_constant__ PadCopies jobs) {
   const PadCopy& j = jobs.job[blockIdx.y];
   if (j.elem_bytes == 2) pad_copy<uint16_t>(j);
