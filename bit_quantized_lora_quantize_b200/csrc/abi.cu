@@ -230,9 +230,10 @@ bool make_map_nd(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
 namespace qlora {
 namespace {
 
-// The dropped copy of X that a linear with adapter dropout keeps at the end of
-// its workspace.
+// What a linear with adapter dropout keeps at the end of its workspace: the
+// dropped copy of X, and in the backward dY W' in float32.
 size_t masked_bytes(int64_t M, int64_t K) { return round_up(static_cast<size_t>(M) * K * 2, 256); }
+size_t dropout_bytes(int64_t M, int64_t K) { return masked_bytes(M, K) + static_cast<size_t>(M) * K * 4; }
 
 // keep * X: the gain goes into the LoRA scale, so that nothing is rounded.
 cudaError_t launch_masked(const uint16_t* X, uint16_t* Xm, int64_t M, int64_t K, const DropArgs& drop,
@@ -266,7 +267,7 @@ qlora_status linear_fwd(const uint16_t* X, int64_t M, int64_t K, int64_t N, cons
       (reinterpret_cast<uintptr_t>(absmax_scale) & 3u))
     return QLORA_ERR_ALIGNMENT;
   const WsLayout wl = ws_layout(M, K, N, r);
-  if (!workspace || ws_bytes < wl.total + (drop ? masked_bytes(M, K) : 0)) return QLORA_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < wl.total + (drop ? dropout_bytes(M, K) : 0)) return QLORA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int* status = reinterpret_cast<int*>(ws);
@@ -345,7 +346,7 @@ qlora_status linear_bwd(const uint16_t* dY, const uint16_t* X, const float* T_sa
       (reinterpret_cast<uintptr_t>(absmax_scale) & 3u))
     return QLORA_ERR_ALIGNMENT;
   const WsLayout wl = ws_layout(M, K, N, r);
-  if (!workspace || ws_bytes < wl.total + (drop ? masked_bytes(M, K) : 0)) return QLORA_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < wl.total + (drop ? dropout_bytes(M, K) : 0)) return QLORA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QLORA_ERR_ALIGNMENT;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int* status = reinterpret_cast<int*>(ws);
@@ -378,8 +379,10 @@ qlora_status linear_bwd(const uint16_t* dY, const uint16_t* X, const float* T_sa
   // the last wave of tiles leaves idle.
   // With adapter dropout dA reads the dropped copy of X, drawn again, and the
   // adapter's part of dX is added by a third launch: its mask differs per
-  // element, so it cannot share the accumulators of dY W'.
+  // element, so it cannot share the accumulators of dY W'.  Those come out in
+  // float32, so that dX is rounded once, as without the dropout.
   const uint16_t* Xa = X;
+  float* base = drop ? reinterpret_cast<float*>(ws + wl.total + masked_bytes(M, K)) : nullptr;
   if (drop) {
     uint16_t* Xm = reinterpret_cast<uint16_t*>(ws + wl.total);
     ProfScope p0(st, "dropout", 1);
@@ -391,11 +394,11 @@ qlora_status linear_bwd(const uint16_t* dY, const uint16_t* X, const float* T_sa
   ProfScope p2(st, "fused_nf4_dx", 1);
   e = launch_fused_dx(dY, codes, absmax_q, absmax_scale, Upair, Ak, M, K, N, r8, dX, status, P, st, Bk,
                       drop ? scale * drop->gain : scale, reinterpret_cast<int*>(ws + wl.cd_off), Xa, Tk, Tpair, dAk,
-                      dBk, !drop);
+                      dBk, base);
   p2.done();
   if (e == cudaSuccess && drop) {
     ProfScope p3(st, "adapter_dx", 1);
-    e = launch_adapter_dx(Upair, Ak, dX, M, K, r8, *drop, st);
+    e = launch_adapter_dx(Upair, Ak, base, dX, M, K, r8, *drop, st);
     p3.done();
   }
   if (e == cudaSuccess && r8 != r) e = launch_pad_copies({{dAk, K, r8, dA, K, r, 4}, {dBk, r8, N, dB, r, N, 4}}, st);
@@ -517,7 +520,7 @@ qlora_status qlora_linear_bwd_dropout(const uint16_t* dY, const uint16_t* X, con
 
 size_t qlora_dropout_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t r) {
   if (check_linear_shape(M, K, N, r) != QLORA_OK || M > kMaxRowElements / K) return 0;
-  return ws_layout(M, K, N, r).total + masked_bytes(M, K);
+  return ws_layout(M, K, N, r).total + dropout_bytes(M, K);
 }
 
 qlora_status qlora_silu_gate_fwd(const uint16_t* G, const uint16_t* U, uint16_t* H, int64_t n, void* stream) {

@@ -1,11 +1,13 @@
 // The adapter's part of the input gradient under adapter dropout:
-//   dX[m, k] += keep[m, k] * sum_j U[m, j] A[k, j]
-// (U carries the LoRA scale and the dropout's gain; the mask is drawn again).
+//   dX[m, k] = bf16(base[m, k] + keep[m, k] * sum_j U[m, j] A[k, j])
+// (base is dY W' as the GEMM accumulated it, in float32, so that dX is rounded
+// once; U carries the LoRA scale and the dropout's gain; the mask is drawn again).
+// Base lies as groups of eight columns, [K / 8][M][8]: the GEMM's lanes hold one
+// row each, so a warp of them writes whole lines.
 //
-// A pass over dX: 4 bytes of HBM traffic per element against 4 r operations,
-// so HBM would allow 20.5 us for 4096 x 8192 at rank 64; measured 49 us (bound
-// by instructions: the draws and the register-fragment products of mma.sync,
-// about 200 per group of eight), a seventh of the input-gradient GEMM of
+// A pass over dX: 6 bytes of HBM traffic per element against 4 r operations,
+// so HBM would allow 30.7 us for 4096 x 8192 at rank 64; measured 56 us (50 with
+// base in bf16, which rounds dX twice), a seventh of the input-gradient GEMM of
 // an 8192 x 8192 layer before it.  A block takes a 64 x 128 tile; U enters as its
 // bf16 pair (hi + lo, about 16 significant bits), 64 ranks at a time by
 // asynchronous copies.
@@ -61,8 +63,9 @@ __device__ __forceinline__ uint32_t a_offset(int row, int c) {
 }
 
 __global__ void __launch_bounds__(kThreads, 3)
-    adapter_dx_kernel(const uint16_t* __restrict__ U, const uint16_t* __restrict__ A, uint16_t* __restrict__ dX,
-                      int64_t M, int64_t K, int r, int rp, const DropArgs d) {
+    adapter_dx_kernel(const uint16_t* __restrict__ U, const uint16_t* __restrict__ A, const float* __restrict__ base,
+                      uint16_t* __restrict__ dX, int64_t M, int64_t base_rows, int64_t K, int r, int rp,
+                      const DropArgs d) {
   __shared__ __align__(1024) uint8_t smem[2 * kUBytes + kABytes];
   const uint32_t s_hi = smem_u32(smem), s_lo = s_hi + kUBytes, s_a = s_lo + kUBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -146,40 +149,40 @@ __global__ void __launch_bounds__(kThreads, 3)
   // This lane's groups of eight: rows wm + 16 i + 8 h + lane / 4, columns
   // wn + 8 (lane % 4).  K % 64 == 0, so a group is whole or outside.  Three
   // blocks per SM hide these loads and the draws better than registers held
-  // for them across the products did (4096 x 8192 at rank 64: 49 us, 57 with
-  // two blocks).
+  // for them across the products did (4096 x 8192 at rank 64, with base in bf16:
+  // 49 us, 57 with two blocks).
   const int64_t k = k0 + wn + 8 * (lane & 3);
   const int row0 = wm + (lane >> 2);
   if (k >= K) return;
   uint16_t* at = dX + (m0 + row0) * K + k;
+  const float* from = base + (k / 8 * base_rows + m0 + row0) * 8;
   uint64_t counter = drop_base(d) + (m0 + row0) * d.groups + k / 8;
   const int64_t step = 8 * K, steps = 8 * d.groups;
-  uint4 old[2][2];
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
-    if (row0 + 8 * n < rows_m) old[n >> 1][n & 1] = __ldcs(reinterpret_cast<const uint4*>(at + n * step));
+  for (int i = 0; i < 2; ++i) {
+    Raw8<float> x[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int h = 0; h < 2; ++h)
+      if (row0 + 16 * i + 8 * h < rows_m) x[h] = load_group_stream(from + (2 * i + h) * 64);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (row0 + 16 * i + 8 * h < rows_m) {
         const KeepGroup keep = keep_group(d, counter);
-        Raw8<__nv_bfloat16> x;
-        x.w[0] = old[i][h].x; x.w[1] = old[i][h].y; x.w[2] = old[i][h].z; x.w[3] = old[i][h].w;
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = raw_f32(x, e) + (keep(e) ? acc[i][e >> 1][2 * h + (e & 1)] : 0.0f);
+        for (int e = 0; e < 8; ++e) v[e] = raw_f32(x[h], e) + (keep(e) ? acc[i][e >> 1][2 * h + (e & 1)] : 0.0f);
         store_group_stream(reinterpret_cast<__nv_bfloat16*>(at), raw_from<__nv_bfloat16>(v));
       }
       at += step;
       counter += steps;
     }
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_adapter_dx(const uint16_t* Upair, const uint16_t* A, uint16_t* dX, int64_t M, int64_t K, int r,
-                              const DropArgs& d, cudaStream_t stream) {
+cudaError_t launch_adapter_dx(const uint16_t* Upair, const uint16_t* A, const float* base, uint16_t* dX, int64_t M,
+                              int64_t K, int r, const DropArgs& d, cudaStream_t stream) {
   // Row blocks beyond a grid's second dimension go to further launches.
   constexpr int64_t kMaxRowBlocks = 65535;
   const int64_t row_blocks = (M + kTileM - 1) / kTileM;
@@ -196,8 +199,8 @@ cudaError_t launch_adapter_dx(const uint16_t* Upair, const uint16_t* A, uint16_t
     cudaLaunchAttribute attr = pdl_attribute();
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, adapter_dx_kernel, Upair + m0 * 2 * lora_pad(r), A, dX + m0 * K,
-                                             M - m0, K, r, lora_pad(r), part);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, adapter_dx_kernel, Upair + m0 * 2 * lora_pad(r), A, base + m0 * 8,
+                                             dX + m0 * K, M - m0, M, K, r, lora_pad(r), part);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -94,6 +94,7 @@ struct PairArgs {
   int rows, cols;   // output extent
   int64_t ld_out;
   uint16_t* out;
+  float* out_f32;   // the output unrounded instead of `out`, or null: [cols / 8][rows][8]
   const uint8_t* absmax_q;
   const float* absmax_scale;
   int64_t w_rows, w_cols;  // N, K of the packed weight
@@ -664,7 +665,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               const int col = col0 + g * 8;
-              if (col < args.cols) {
+              if (col < args.cols && args.out_f32) {
+                uint4* to = reinterpret_cast<uint4*>(args.out_f32 + (static_cast<int64_t>(col >> 3) * args.rows + row) * 8);
+                to[0] = make_uint4(v[g * 8], v[g * 8 + 1], v[g * 8 + 2], v[g * 8 + 3]);
+                to[1] = make_uint4(v[g * 8 + 4], v[g * 8 + 5], v[g * 8 + 6], v[g * 8 + 7]);
+              } else if (col < args.cols) {
                 uint32_t p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -820,7 +825,7 @@ cudaError_t launch_fused_dx(const uint16_t* dY, const uint8_t* codes, const uint
                             const float* absmax_scale, uint16_t* Upair, const uint16_t* A, int64_t M, int64_t K,
                             int64_t N, int r, uint16_t* dX, int* status, const Nf4Params& P, cudaStream_t stream,
                             const uint16_t* B, float scale, int* ctr, const uint16_t* X, const float* T_save,
-                            uint16_t* Tpair, float* dA, float* dB, bool lora_stages) {
+                            uint16_t* Tpair, float* dA, float* dB, float* base) {
   const int rp = lora_pad(r);
   CUtensorMap mD, mC, mU, mA, mR;
   if (!make_map_2d(&mD, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dY, N, M, N * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -867,12 +872,13 @@ cudaError_t launch_fused_dx(const uint16_t* dY, const uint8_t* codes, const uint
     args.t_pair = Tpair;
   }
   args.nkb = static_cast<int>((N + 63) / 64);
-  args.lora_kb = lora_stages ? 2 * rp / 64 : 0;
+  args.lora_kb = base ? 0 : 2 * rp / 64;
   args.lora_mod = rp;
   args.rows = static_cast<int>(M);
   args.cols = static_cast<int>(K);
   args.ld_out = K;
   args.out = dX;
+  args.out_f32 = base;
   args.absmax_q = absmax_q;
   args.absmax_scale = absmax_scale;
   args.w_rows = N;

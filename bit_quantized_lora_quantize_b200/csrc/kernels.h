@@ -83,14 +83,15 @@ cudaError_t launch_fused_fwd(const uint16_t* X, const uint8_t* codes, const uint
 // With `ctr` the kernel also computes U = s dY B^T (its pair in Upair) the
 // same way, and, when dA and dB are given, dA = X^T U and dB = T^T dY (the
 // rank units write the bf16 pair of T_save into Tpair for that); with
-// ctr == nullptr Upair comes from the previous kernel.  Without `lora_stages`
-// dX is dY W' alone (the caller adds the adapter's part from Upair).
+// ctr == nullptr Upair comes from the previous kernel.  With `base` the launch
+// leaves dY W' alone there, float32 [K / 8][M][8], and dX untouched (the caller
+// adds the adapter's part from Upair and rounds).
 cudaError_t launch_fused_dx(const uint16_t* dY, const uint8_t* codes, const uint8_t* absmax_q,
                             const float* absmax_scale, uint16_t* Upair, const uint16_t* A, int64_t M, int64_t K,
                             int64_t N, int r, uint16_t* dX, int* status, const Nf4Params& P, cudaStream_t stream,
                             const uint16_t* B = nullptr, float scale = 0.0f, int* ctr = nullptr,
                             const uint16_t* X = nullptr, const float* T_save = nullptr, uint16_t* Tpair = nullptr,
-                            float* dA = nullptr, float* dB = nullptr, bool lora_stages = true);
+                            float* dA = nullptr, float* dB = nullptr, float* base = nullptr);
 
 // Counter ints one fused launch with rank units needs for M rows.
 int fused_ctr_ints(int64_t M);

@@ -75,9 +75,9 @@ inline bool make_drop_args(double p, uint64_t seed, uint64_t offset, const uint6
 cudaError_t launch_dropout(int32_t dtype, const void* X, const void* residual, void* Y, int64_t rows, int64_t cols,
                            const DropArgs& d, cudaStream_t stream);
 
-// dX += keep * (U A^T): U as its bf16 pair [M x 2 rp], A [K x r] with r a
-// multiple of 8, dX bf16 [M x K].
-cudaError_t launch_adapter_dx(const uint16_t* Upair, const uint16_t* A, uint16_t* dX, int64_t M, int64_t K, int r,
-                              const DropArgs& d, cudaStream_t stream);
+// dX = bf16(base + keep * (U A^T)): U as its bf16 pair [M x 2 rp], A [K x r] with
+// r a multiple of 8, base float32 [K / 8][M][8], dX bf16 [M x K].
+cudaError_t launch_adapter_dx(const uint16_t* Upair, const uint16_t* A, const float* base, uint16_t* dX, int64_t M,
+                              int64_t K, int r, const DropArgs& d, cudaStream_t stream);
 
 }  // namespace qlora

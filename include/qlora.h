@@ -325,17 +325,17 @@ QLORA_API qlora_status qlora_dropout_bwd(const void* dY, void* dX, int64_t rows,
  * reads X as it is):
  *   Y  = bf16(X W'^T + T B),      T_save = s (dropout(X) A)
  *   U  = s dY B^T,  dB = T_save^T dY,  dA = dropout(X)^T U,
- *   dX = dY W' + keep * c (U A^T)
+ *   dX = bf16(dY W' + keep * c (U A^T))
  * with the draws of qlora_dropout_fwd for rows = M, cols = K; the backward
  * takes the forward's p, seed, offset and counter and draws the mask again.
  * The gain c is applied in float32 to the rank-r intermediates, so the
- * dropped inputs take no rounding of their own.  dX is rounded to bf16 twice:
- * dY W', then its sum with the adapter's part.
+ * dropped inputs take no rounding of their own, and dX, like Y, is rounded to
+ * bf16 once.
  * Same supported shapes, code values, buffers and workspace rule as
  * qlora_linear_fwd_4bit / qlora_linear_bwd_4bit, with a workspace of at least
- * qlora_dropout_workspace_bytes bytes (it holds a dropped copy of X during a
- * call, besides what the plain calls keep there).  Every M runs the pair
- * GEMMs of the large-M calls.  s * c must be finite
+ * qlora_dropout_workspace_bytes bytes (during a call it holds a dropped copy of
+ * X and, in float32, dY W', besides what the plain calls keep there).  Every M
+ * runs the pair GEMMs of the large-M calls.  s * c must be finite
  * (QLORA_ERR_INVALID_ARG), M * K at most 2^40.
  */
 QLORA_API qlora_status qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,

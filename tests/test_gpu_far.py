@@ -105,3 +105,20 @@ def test_linear_with_adapter_dropout():
     dx, _, _ = q.qlora_linear_bwd_dropout(dY[-TAIL:].clone(), tail, t, W, A, B, 2.0, p, 9, 5 + first)
     close(dX[-TAIL:], dx, float(dx.abs().max()) * 2 * HALF)
     assert bool(dA.isfinite().all() and dB.isfinite().all())
+
+
+def test_adapter_dropout_rows_past_one_grid():
+    """More 64-row blocks than a grid's second dimension holds: the rows of the
+    second launch come out bit for bit as they do alone (every row's sums are
+    taken in the same order at any M)."""
+    edge = 65535 * 64
+    M, K, N, r, p, cut = edge + 300, 64, 64, 8, 0.3, edge - 200
+    X, dY, T = far(M, K), far(M, N, 1), torch.randn(M, r, device="cuda")
+    W = q.qlora_quantize_nf4(far(N, K, 2) * 0.05)
+    A, B = far(K, r, 3) * 0.01, far(r, N, 4) * 0.1
+    dX, _, _ = q.qlora_linear_bwd_dropout(dY, X, T, W, A, B, 2.0, p, 9, 5)
+    alone, _, _ = q.qlora_linear_bwd_dropout(dY[cut:].clone(), X[cut:].clone(), T[cut:].clone(), W, A, B, 2.0, p, 9,
+                                             5 + cut * (K // 8))
+    assert torch.equal(dX[cut:], alone)
+    first, _, _ = q.qlora_linear_bwd_dropout(dY[:512].clone(), X[:512].clone(), T[:512].clone(), W, A, B, 2.0, p, 9, 5)
+    assert torch.equal(dX[:512], first)

@@ -172,3 +172,22 @@ def test_gradients_against_differences():
             if name == "dB" else 0.0
         tol = 1.01 * float((bounds[name][1] * np.abs(d)).sum()) + extra + 1e-6 * abs(diff) + 1e-6
         assert abs(float((f64(grads[k]) * d).sum()) - diff) <= tol, name
+
+
+@pytest.mark.parametrize("M,K,N,r,p", [(16, 256, 256, 8, 0.05), (150, 256, 264, 12, 0.1), (300, 512, 520, 64, 0.0),
+                                       (700, 576, 136, 130, 0.5)])
+def test_dx_is_rounded_once(M, K, N, r, p):
+    """dX holds bf16 of one float32 sum: besides the float32 sums' own error
+    (acc) it is within half a step, not a whole one."""
+    case = synthetic.linear_case(M, K, N, r, 1.0, seed=M + r)
+    Wp = q.qlora_quantize_nf4(case.W.to(DEV))
+    X, A, B, dY = (t.to(DEV) for t in (case.X, case.A, case.B, case.dY))
+    _, T = q.qlora_linear_fwd_dropout(X, Wp, A, B, 1.0, p, 77, 5)
+    dX, _, _ = q.qlora_linear_bwd_dropout(dY, X, T, Wp, A, B, 1.0, p, 77, 5)
+    a, dy, w, la, lb = np.abs, f64(dY), f64(q.qlora_dequantize_nf4(Wp)), f64(A), f64(B)
+    u, gain = dy @ lb.T, dropout_gain(p)
+    add = np.where(dropout_keep(M, K, p, 77, 5), gain * (u @ la.T), 0.0)
+    ref = dy @ w + add
+    eu = acc(N, a(dy) @ a(lb.T)) + (4 * U + H * H) * a(u)  # U's own sum, its scale and its bf16 pair
+    err = acc(N, a(dy) @ a(w)) + gain * (eu @ a(la.T) + acc(2 * r, a(u) @ a(la.T))) + 4 * U * (a(add) + a(ref))
+    check(dX, ref, err + H * (a(ref) + err), "dX")
