@@ -17,6 +17,7 @@
 #include "abi_internal.h"
 #include "kernels.h"
 #include "nf4_host.h"
+#include "ptx.cuh"
 #include "rows_host.h"
 #include "tensor_map.h"
 
@@ -548,14 +549,18 @@ qlora_status qlora_check_status(void* workspace, void* stream) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e);
-  bool timed_out = false;
+  bool timed_out = false, overlapped = false;
+  const auto look = [&](int word) {
+    overlapped |= word == kStatusOverlap;
+    timed_out |= word != 0 && word != kStatusOverlap;
+  };
   if (workspace) {
     int word = 0;
     e = cudaMemcpyAsync(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(e);
+    look(word);
     if (word != 0) {
-      timed_out = true;
       e = cudaMemsetAsync(workspace, 0, sizeof(int), st);
       if (e == cudaSuccess) e = cudaStreamSynchronize(st);
       if (e != cudaSuccess) return cuda_fail(e);
@@ -566,11 +571,11 @@ qlora_status qlora_check_status(void* workspace, void* stream) {
   int word = 0;
   e = codec_status_take(st, &word);
   if (e != cudaSuccess) return cuda_fail(e);
-  timed_out |= word != 0;
+  look(word);
   e = noalloc_status_take(st, &word);
   if (e != cudaSuccess) return cuda_fail(e);
-  timed_out |= word != 0;
-  return timed_out ? QLORA_ERR_TIMEOUT : QLORA_OK;
+  look(word);
+  return overlapped ? QLORA_ERR_OVERLAP : timed_out ? QLORA_ERR_TIMEOUT : QLORA_OK;
 }
 
 qlora_status qlora_set_wait_timeout(uint64_t timeout_ns) {
@@ -603,6 +608,7 @@ const char* qlora_status_string(qlora_status s) {
     case QLORA_ERR_WORKSPACE: return "workspace missing or too small";
     case QLORA_ERR_CUDA: return "CUDA error";
     case QLORA_ERR_TIMEOUT: return "kernel pipeline wait timed out";
+    case QLORA_ERR_OVERLAP: return "calls overlapped on one workspace";
   }
   return "unknown status";
 }

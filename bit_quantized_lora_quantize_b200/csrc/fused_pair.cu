@@ -222,8 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (args.ctr) {
     unit = rank == 0 ? *unit_slot : ld_cluster_s32(map_rank(unit_slot, 0));
     // Tickets past the last come only from a second call that runs on the same
-    // workspace: its results are lost, but it stays inside its tensors.
-    unit = min(unit, args.units - 1);
+    // workspace: results of both may be lost, which the status word tells, but
+    // every access stays inside its tensors.
+    if (unit >= args.units) {
+      if (threadIdx.x == 0 && rank == 0 && args.status) atomicCAS(args.status, 0, kStatusOverlap);
+      unit = args.units - 1;
+    }
   }
   // Ticket order: rank units; tiles [0, early); tail units [0, t_first);
   // the other tiles; the other tail units.
@@ -703,6 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // taken its ticket and is past its last look at a ready count.
     __threadfence();
     if (atomicAdd(args.ctr + 1, 1) == args.units - 1) {
+      // More tickets than units: pairs of another call took some of them.
+      if (*static_cast<volatile int*>(args.ctr) != args.units && args.status)
+        atomicCAS(args.status, 0, kStatusOverlap);
       for (int m = 0; m < args.r_units; ++m) args.ctr[2 + m] = 0;
       args.ctr[0] = 0;
       args.ctr[1] = 0;

@@ -79,6 +79,11 @@ constexpr uint64_t kDrainTimeoutNs = 2000000ull;    // 2 ms
 // timer after every try, so that short limits are honoured.
 constexpr uint64_t kShortWaitNs = 1000000ull;
 
+// Values of a status word: a wait that gave up (plus its site), and a launch
+// that found another one at work on its workspace.
+constexpr int kStatusTimeout = 0x100;
+constexpr int kStatusOverlap = 0x200;
+
 struct WaitCtx {
   volatile int* abort_flag;  // shared
   int* status;               // global, may be null
@@ -88,7 +93,7 @@ struct WaitCtx {
 
 __device__ __forceinline__ bool wait_gave_up(const WaitCtx& ctx) {
   *ctx.abort_flag = 1;
-  if (ctx.status) atomicCAS(ctx.status, 0, 0x100 + ctx.site);
+  if (ctx.status) atomicCAS(ctx.status, 0, kStatusTimeout + ctx.site);
   return false;
 }
 

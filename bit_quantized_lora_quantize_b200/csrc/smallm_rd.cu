@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::offAbort);
   float* lvl2 = reinterpret_cast<float*>(sm + L::offLvl);
   if (smem_u32(sm) != kSmemBase) {  // table addressing and 1024-byte aligned swizzled copies rely on it
-    if (tid == 0 && a.status) atomicCAS(a.status, 0, 0x100 + 62);
+    if (tid == 0 && a.status) atomicCAS(a.status, 0, kStatusTimeout + 62);
     return;
   }
 

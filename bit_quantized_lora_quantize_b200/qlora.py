@@ -23,7 +23,7 @@ QLORA_OK = 0
 CODES = {"nf4": 0, "fp4": 1, "int4": 2}
 DQ = {"linear8": 0, "centred_fp8": 0x100}
 STATUS_NAMES = {0: "QLORA_OK", 1: "QLORA_ERR_INVALID_ARG", 2: "QLORA_ERR_ALIGNMENT", 3: "QLORA_ERR_UNSUPPORTED",
-                4: "QLORA_ERR_WORKSPACE", 5: "QLORA_ERR_CUDA", 6: "QLORA_ERR_TIMEOUT"}
+                4: "QLORA_ERR_WORKSPACE", 5: "QLORA_ERR_CUDA", 6: "QLORA_ERR_TIMEOUT", 7: "QLORA_ERR_OVERLAP"}
 
 # Exported symbols and their C signatures.
 _P = ctypes.c_void_p
@@ -343,8 +343,9 @@ def qlora_silu_gate_bwd(G: torch.Tensor, U: torch.Tensor, dH: torch.Tensor, dG: 
 
 def qlora_check_status(workspace: torch.Tensor | None = None) -> int:
     """Synchronise and return the device status code (0 = OK, 6 = a pipeline
-    wait timed out): the workspace's word (if given) and the library's own
-    words for the calls without a workspace."""
+    wait timed out, 7 = linear calls overlapped on one workspace): the
+    workspace's word (if given) and the library's own words for the calls
+    without a workspace."""
     return int(lib().qlora_check_status(_ptr(workspace) if workspace is not None else None, _stream()))
 
 

@@ -68,7 +68,8 @@ typedef enum {
   QLORA_ERR_UNSUPPORTED = 3, /* a shape outside the supported set (see each call) */
   QLORA_ERR_WORKSPACE = 4,   /* workspace pointer null or smaller than qlora_workspace_bytes */
   QLORA_ERR_CUDA = 5,        /* a CUDA launch or query failed */
-  QLORA_ERR_TIMEOUT = 6      /* a kernel gave up waiting on a pipeline barrier (qlora_check_status) */
+  QLORA_ERR_TIMEOUT = 6,     /* a kernel gave up waiting on a pipeline barrier (qlora_check_status) */
+  QLORA_ERR_OVERLAP = 7      /* linear calls overlapped on one workspace (qlora_check_status) */
 } qlora_status;
 
 /*
@@ -164,9 +165,12 @@ QLORA_API qlora_status qlora_dequantize_4bit(const uint8_t* codes, const uint8_t
  *                 bytes, filled with zeros once before its first use.  It
  *                 holds the status word read by qlora_check_status (first
  *                 256 bytes) and counters that every call leaves at zero;
- *                 everything else is overwritten before it is read.  After
- *                 qlora_check_status reports QLORA_ERR_TIMEOUT, fill it with
- *                 zeros again before the next call.
+ *                 everything else is overwritten before it is read.  Calls
+ *                 that may overlap on the GPU need one each: results of calls
+ *                 that share one are undefined, and where a GEMM of the large-M
+ *                 calls finds another one at work, qlora_check_status reports
+ *                 QLORA_ERR_OVERLAP.  After that or QLORA_ERR_TIMEOUT, fill it
+ *                 with zeros again before the next call.
  * Supported: K % 64 == 0, N % 8 == 0 (the weight's blocks and the row
  * strides of Y, dY and B, which are copied by TMA, in 16-byte units),
  * 1 <= r <= 256, M, N, K < 2^31.  Otherwise QLORA_ERR_UNSUPPORTED.  Ranks
@@ -256,7 +260,8 @@ QLORA_API qlora_status qlora_linear_bwd_4bit(const uint16_t* dY, const uint16_t*
  *     first call before any stream capture on that device.
  *   - All calls on a device share the array.  Calls that may overlap on the
  *     GPU (other streams, or host threads without ordering) race and must be
- *     serialised by the caller.
+ *     serialised by the caller (qlora_check_status reports QLORA_ERR_OVERLAP
+ *     where a launch finds another one at work).
  *   - Each call clears the counters it uses.  A pipeline wait that gives up
  *     sets the array's status word, which stays set until
  *     qlora_check_status(NULL, stream) (or with any workspace) on that device
@@ -480,8 +485,9 @@ QLORA_API size_t qlora_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t 
  * of `workspace` (skipped when workspace is NULL) and the two the library
  * keeps on the current device for calls that take no workspace
  * (qlora_quantize_nf4 and qlora_linear_fwd_noalloc).  Returns QLORA_OK, or
- * QLORA_ERR_TIMEOUT if a kernel of an earlier call gave up on a pipeline wait
- * (its outputs are then undefined).  Every word read is reset to zero. */
+ * QLORA_ERR_TIMEOUT if a kernel of an earlier call gave up on a pipeline wait,
+ * or QLORA_ERR_OVERLAP if linear calls ran at the same time on one workspace
+ * (outputs are then undefined).  Every word read is reset to zero. */
 QLORA_API qlora_status qlora_check_status(void* workspace, void* stream);
 
 /* Limit of every bounded wait inside the kernels (a pipeline barrier, a

@@ -92,3 +92,36 @@ def test_codec_status_is_clear_after_normal_calls():
     Wp = q.qlora_quantize_nf4(W)
     q.qlora_dequantize_nf4(Wp)
     assert q.qlora_check_status(None) == 0
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+def test_tickets_of_another_call_are_reported(which):
+    """A GEMM that finds another call at work on its workspace (its tickets taken
+    and its row blocks marked ready, set by hand here) leaves outputs unwritten:
+    the status word says so, and a zero-filled workspace works again."""
+    case = synthetic.linear_case(1100, 512, 640, 64, 0.25, seed=42)
+    Wp = q.qlora_quantize_nf4(case.W.to(DEV))
+    X, A, B, dY = (t.to(DEV) for t in (case.X, case.A, case.B, case.dY))
+    ws = q.new_workspace(case.M, case.K, case.N, case.r, DEV)
+    Y, T = q.qlora_linear_fwd(X, Wp, A, B, case.scale, workspace=ws)
+    dX, dA, dB = q.qlora_linear_bwd(dY, X, T, Wp, A, B, case.scale, workspace=ws)
+    assert q.qlora_check_status(ws) == 0
+    off = counters_offsets(case.M)[0 if which == "fwd" else 1]
+    counters = ws[off:off + 20].view(torch.int32)
+    counters[0], counters[2:] = 1000, 2
+    if which == "fwd":
+        out = torch.full_like(Y, float("nan"))
+        q.qlora_linear_fwd(X, Wp, A, B, case.scale, workspace=ws, Y=out, T_save=T)
+    else:
+        out = torch.full_like(dX, float("nan"))
+        q.qlora_linear_bwd(dY, X, T, Wp, A, B, case.scale, workspace=ws, dX=out)
+    status = q.qlora_check_status(ws)
+    assert out.isnan().any()
+    assert status == 7
+    assert q.qlora_check_status(ws) == 0
+    ws.zero_()
+    again = q.qlora_linear_fwd(X, Wp, A, B, case.scale, workspace=ws)
+    assert torch.equal(again[0], Y)
+    assert all(torch.equal(a, b) for a, b in zip(q.qlora_linear_bwd(dY, X, again[1], Wp, A, B, case.scale, workspace=ws),
+                                                 (dX, dA, dB)))
+    assert q.qlora_check_status(ws) == 0
