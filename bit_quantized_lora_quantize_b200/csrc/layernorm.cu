@@ -358,6 +358,8 @@ struct RowRing {
       bulk_load(dst + (lo - from), reinterpret_cast<const void*>(lo), static_cast<uint32_t>(hi - lo), bar);
   }
   // The elements that load() leaves out, at most seven at each end of the tensor.
+  // A later copy into the same stage, which the same thread starts, overwrites
+  // them: the fence orders these stores before it.
   __device__ __forceinline__ void ends(uint8_t* dst, int64_t at, int64_t n) const {
     uintptr_t lo, hi;
     span(at, n, lo, hi);
@@ -371,6 +373,7 @@ struct RowRing {
       const int64_t tail = min(n, static_cast<int64_t>((e - hi) / sizeof(T)));
       for (int64_t i = n - tail; i < n; ++i) to[i] = base[at + i];
     }
+    if (lo > b || hi < e) fence_proxy_async_smem();
   }
 };
 

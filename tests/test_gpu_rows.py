@@ -351,3 +351,21 @@ def test_norm_on_a_side_stream_and_in_a_graph():
     ref = q.qlora_layernorm_fwd(X, w)
     ref_b = q.qlora_layernorm_bwd(dY, X, ref[1], ref[2], w)
     assert all(torch.equal(a, b) for a, b in zip((Y, mean, rstd, dX, dw, db), ref + ref_b))
+
+
+@pytest.mark.parametrize("rows,cols,pad", [(12000, 1000, 1), (6000, 2047, 5), (2000, 5003, 3), (12000, 520, 7)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_layernorm_backward_past_the_ring_unaligned(rows, cols, pad, dtype):
+    """Tensors that start off a 16-byte boundary, with rows enough for every
+    stage of the ring to be filled many times: the first stage once holds
+    elements that ordinary stores put there."""
+    t = TYPES[dtype]
+    X, dY = rand(rows, cols, t, 1, mean=0.3, std=2.0, pad=pad), rand(rows, cols, t, 2, pad=pad)
+    _, mean, rstd = q.qlora_layernorm_fwd(X)
+    got = q.qlora_layernorm_bwd(dY, X, mean, rstd)
+    x, dy, m, r = f64(X), f64(dY), f64(mean), f64(rstd)
+    refs = layernorm_grads(dy, x, m, r)
+    for name, a, ref, bound in zip(("dX", "dweight", "dbias"), got, refs,
+                                   bwd_bounds(dy, x, m, r, None, refs[0], rows, cols, t)):
+        check(a, ref, bound, name)
+    assert all(torch.equal(a, b) for a, b in zip(got, q.qlora_layernorm_bwd(dY, X, mean, rstd)))
