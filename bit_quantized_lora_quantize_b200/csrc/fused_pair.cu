@@ -725,8 +725,7 @@ cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& c, const CUtens
   using L = PairSmem<MNB>;
   static_assert(L::kDynamic <= 232448, "shared memory budget");
   auto kern = fused_pair_kernel<MNB>;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_shared_memory(kern, L::kDynamic, done);
+  const cudaError_t e = allow_shared_memory(kern, L::kDynamic);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * args.units), 1, 1);

@@ -722,8 +722,7 @@ cudaError_t launch_pair_gemm(const CUtensorMap& x, const CUtensorMap& w, const P
   static_assert(L::kDynamic <= 232448, "shared memory budget");
   static_assert(L::offBar % 8 == 0 && L::offScale % 16 == 0, "barriers, and scales read as vectors");
   auto kern = pair_kernel<T, SPLIT>;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_shared_memory(kern, L::kDynamic, done);
+  const cudaError_t e = allow_shared_memory(kern, L::kDynamic);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);

@@ -2,7 +2,6 @@
 // the kernels.  Not part of the public header.
 #pragma once
 
-#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <initializer_list>
@@ -23,18 +22,12 @@ uint64_t wait_limit_ns();
 int device_sm_count();
 int device_l2_bytes();
 
-// Opt a kernel in to `bytes` of dynamic shared memory on the current device,
-// once per kernel and device.
+// Opt a kernel in to `bytes` of dynamic shared memory.  The attribute belongs to
+// the current context, of which a process may have several, one after the other
+// (a device reset) or at once, so every launch sets it.
 template <typename Kernel>
-cudaError_t allow_shared_memory(Kernel* kern, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
+cudaError_t allow_shared_memory(Kernel* kern, int bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 // Status words the library keeps on the device for calls without a

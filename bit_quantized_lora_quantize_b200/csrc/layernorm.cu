@@ -859,8 +859,7 @@ cudaError_t launch_ln_fwd(const LnFwdArgs& a, const DropArgs* drop, int32_t dtyp
 template <typename T, typename W, int VEC, bool FUSED, int R>
 cudaError_t launch_bwd_rows(const LnBwdArgs& a, int grid, size_t smem, cudaStream_t stream) {
   auto kern = ln_bwd_kernel<T, W, VEC, FUSED, R>;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_shared_memory(kern, kRingBytes, done);
+  const cudaError_t e = allow_shared_memory(kern, kRingBytes);
   if (e != cudaSuccess) return e;
   kern<<<grid, kBwdThreads, smem, stream>>>(a);
   return cudaGetLastError();
