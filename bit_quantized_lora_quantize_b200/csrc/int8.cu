@@ -4,8 +4,9 @@
 //   s_row = fp32(max|x| / 127),  code = x / s_row to the nearest whole number
 //   (ties to even, of the real quotient),  Y = sx[m] sw[n] sum_k xq[m,k] wq[n,k]
 //
-// Sums are exact in 32-bit integers (depth up to 133144), so no split of the
-// depth and no order of work changes a result; float32 enters in the epilogue.
+// Sums are exact in 32-bit integers (codes in -127 .. 127, depth up to 133144),
+// so no split of the depth and no order of work changes a result; float32
+// enters in the epilogue.
 //
 // Three kernels:
 // - quantization: one pass, rows in registers, HBM-bound (4096 x 8192 in bf16
@@ -40,7 +41,7 @@ namespace qlora {
 namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr int64_t kMaxDepth = 2147483647 / (127 * 127);  // int32 sums stay exact
+constexpr int64_t kMaxDepth = 2147483647 / (127 * 127);  // int32 sums of codes in -127 .. 127 stay exact
 constexpr int kDepth = 128;                              // bytes of K per stage: one swizzle row
 
 // ================================================================ quantization

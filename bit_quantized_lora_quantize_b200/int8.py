@@ -19,7 +19,7 @@ class PackedInt8:
     """A matrix [rows, cols] as 8-bit codes with one scale per row.  Rows of
     codes lie ``codes.stride(0)`` bytes apart, a multiple of 16."""
 
-    codes: torch.Tensor  # int8 [rows, ld], ld >= cols
+    codes: torch.Tensor  # int8 [rows, ld], ld >= cols; -127..127 (-128 only up to 131071 columns)
     scale: torch.Tensor  # float32 [rows]
     shape: tuple
 

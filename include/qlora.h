@@ -422,8 +422,10 @@ QLORA_API size_t qlora_layernorm_workspace_bytes(int64_t rows, int64_t cols);
  * (QLORA_ERR_INVALID_ARG; rows of codes count from the first to the end of the
  * last).
  * qlora_linear_int8_fwd quantizes X into the workspace and multiplies.
- * M, K, N >= 1, K <= 133144 (sums stay exact in 32 bits), M, N < 2^31 - 2^15;
- * otherwise QLORA_ERR_UNSUPPORTED.  Results do not depend on the order of
+ * M, K, N >= 1, K <= 133144, M, N < 2^31 - 2^15; otherwise
+ * QLORA_ERR_UNSUPPORTED.  Up to that K the sums of codes in -127..127, which
+ * quantization keeps to, are exact in 32 bits; codes of other origin that hold
+ * -128 are good up to K = 131071, which the call cannot check.  Results do not depend on the order of
  * work.  workspace: at least qlora_int8_workspace_bytes bytes, the first 1024
  * filled with zeros once before its first use (status word and counters, which
  * every call leaves at zero); one workspace may serve calls of several sizes in

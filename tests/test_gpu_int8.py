@@ -182,3 +182,13 @@ def test_captured_token_step_on_a_side_stream():
         torch.cuda.synchronize()
         assert torch.equal(Y, q.qlora_linear_int8_fwd(X, W))
     assert q.qlora_check_status(ws) == 0
+
+
+@pytest.mark.parametrize("M,N", [(1, 40), (100, 130)])
+def test_deepest_sums_of_the_lowest_code(M, N):
+    """-128 everywhere: sums of 2^14 K fit 32 bits up to K = 131071."""
+    K = 131071
+    low = lambda n: q.PackedInt8(torch.full((n, K + 1), -128, dtype=torch.int8, device=DEV),  # noqa: E731
+                                 torch.ones(n, device=DEV), (n, K))
+    Y = q.qlora_matmul_int8(low(M), low(N), torch.float32)
+    assert (Y == float(np.float32(128 * 128 * K))).all()
