@@ -888,7 +888,10 @@ cudaError_t launch_bwd(LnBwdArgs a, bool vec, float* dw, float* db, cudaStream_t
   }
   const int rpi = slots * rows_per_warp;
   const int64_t stage = static_cast<int64_t>(a.tensor_bytes) * (FUSED && a.dz ? 3 : 2);
-  if (a.cols > kBwdCols || a.stages < 2) {
+  // The step loop needs two stages: one tensor's rows of a step are at most
+  // kBwdCols values, whatever the columns.
+  static_assert(2 * 3 * ((kBwdCols * 4 + 15 + 127) / 128 * 128) <= kRingBytes, "two stages fit");
+  if (a.cols > kBwdCols) {
     if (vec) ln_bwd_long_kernel<T, W, kAligned, FUSED><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
     else ln_bwd_long_kernel<T, W, kRagged, FUSED><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
     e = cudaGetLastError();
