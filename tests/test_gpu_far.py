@@ -122,3 +122,51 @@ def test_adapter_dropout_rows_past_one_grid():
     assert torch.equal(dX[cut:], alone)
     first, _, _ = q.qlora_linear_bwd_dropout(dY[:512].clone(), X[:512].clone(), T[:512].clone(), W, A, B, 2.0, p, 9, 5)
     assert torch.equal(dX[:512], first)
+
+
+@pytest.mark.parametrize("cols", [8192, 8191])
+def test_norm_parameter_gradients(cols):
+    """Sums over every row whose terms mostly have one sign, so that rows left out,
+    taken twice or read elsewhere show: the 5712 rows past 2^32 elements are
+    1.1 % of each sum.  A column's sum is a chain over a block's rows (one row
+    slot at these widths), then over slots and blocks; h takes two roundings."""
+    X = far(ROWS, cols)
+    X += 1.0
+    _, mean, rstd = q.qlora_layernorm_fwd(X)
+    _, dw, db = q.qlora_layernorm_bwd(X, X, mean, rstd)
+    want = torch.zeros(4, cols, dtype=torch.float64, device="cuda")  # sums and sums of magnitudes
+    for i in range(0, ROWS, 8192):
+        x = X[i:i + 8192].double()
+        t = x * ((x - mean[i:i + 8192, None]) * rstd[i:i + 8192, None])
+        want += torch.stack([t.sum(0), t.abs().sum(0), x.sum(0), x.abs().sum(0)])
+    blocks = min(torch.cuda.get_device_properties(0).multi_processor_count, 160)
+    slack = (-(-ROWS // blocks) + 16 + 20 + 8 + 5 + 4) * 1.01 * 2.0 ** -24
+    assert bool(((dw - want[0]).abs() <= slack * want[1]).all())
+    assert bool(((db - want[2]).abs() <= slack * want[3]).all())
+    assert float((0.005 * want[0] / want[1]).min()) > slack  # rows left out would show
+
+
+def test_adapter_gradients():
+    """dA and dB of the linear with adapter dropout over 66000 rows of 65536
+    columns, all terms positive: 0.7 % of each sum lies past 2^32 elements.  A
+    tensor-core sum of n products is off by at most (n / 8 + 8) 2^-23 of their
+    magnitudes, the bf16 pairs by 2^-16, U by its own sum."""
+    M, K, N, r, p = 66_000, 65536, 64, 8, 0.3
+    X, dY = far(M, K).abs_(), far(M, N, 4).abs_()
+    W = q.qlora_quantize_nf4(far(N, K, 1) * 0.05)
+    A, B = far(K, r, 2) * 0.01, far(r, N, 3).abs_() * 0.1
+    T = torch.rand(M, r, device="cuda")
+    _, dA, dB = q.qlora_linear_bwd_dropout(dY, X, T, W, A, B, 2.0, p, 9, 5)
+    acc = lambda n: (n / 8 + 8) * 2.0 ** -23  # noqa: E731
+    gain = 65536 / (65536 - round(65536 * p))
+    u = 2.0 * gain * (dY.double() @ B.double().t())
+    want = torch.zeros(K, r, dtype=torch.float64, device="cuda")
+    for i in range(0, M, 4096):
+        x = X[i:i + 4096]
+        kept = q.qlora_dropout_fwd(torch.ones_like(x), p, 9, 5 + i * (K // 8)) != 0
+        want += torch.where(kept, x, 0).double().t() @ u[i:i + 4096]
+    slack = 1.01 * (acc(2 * M) + acc(N) + 2.0 ** -16 + 2.0 ** -22)
+    assert bool(((dA - want).abs() <= slack * want).all())
+    want = T.double().t() @ dY.double()
+    assert bool(((dB - want).abs() <= slack * want).all())
+    assert slack < 0.006

@@ -369,3 +369,57 @@ def test_layernorm_backward_past_the_ring_unaligned(rows, cols, pad, dtype):
                                    bwd_bounds(dy, x, m, r, None, refs[0], rows, cols, t)):
         check(a, ref, bound, name)
     assert all(torch.equal(a, b) for a, b in zip(got, q.qlora_layernorm_bwd(dY, X, mean, rstd)))
+
+
+# ------------------------------------------------------------------ the plans of ordinary training calls
+# Two rows per warp and step, one to sixteen row slots per block, rings that wrap.
+@pytest.mark.parametrize("rows,cols,dtype", [(2500, 4096, "bf16"), (4096, 2048, "fp16"), (6000, 1024, "bf16"),
+                                             (1500, 5120, "fp16"), (20000, 250, "bf16"), (12000, 257, "fp32")])
+def test_layernorm_backward_of_many_rows(rows, cols, dtype):
+    t = TYPES[dtype]
+    X, dY = rand(rows, cols, t, 1, mean=0.3, std=2.0), rand(rows, cols, t, 2)
+    w = rand(1, cols, torch.float32, 5, mean=1.0, std=0.3).view(-1)
+    _, mean, rstd = q.qlora_layernorm_fwd(X, w)
+    ws = q.new_layernorm_workspace(rows, cols, DEV)
+    got = q.qlora_layernorm_bwd(dY, X, mean, rstd, w, workspace=ws)
+    assert q.qlora_check_status(ws) == 0
+    x, dy, m, r, wv = f64(X), f64(dY), f64(mean), f64(rstd), f64(w)
+    refs = layernorm_grads(dy, x, m, r, wv)
+    for name, a, ref, bound in zip(("dX", "dweight", "dbias"), got, refs,
+                                   bwd_bounds(dy, x, m, r, wv, refs[0], rows, cols, t)):
+        check(a, ref, bound, name)
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(1500, 5120, "bf16"), (2500, 2560, "fp16"), (2500, 4096, "bf16"),
+                                             (6000, 1000, "bf16"), (20000, 250, "fp16")])
+@pytest.mark.parametrize("with_dz", [True, False])
+def test_fused_backward_of_many_rows(rows, cols, dtype, with_dz):
+    t, p, seed, offset = TYPES[dtype], 0.2, 77, 1 << 33
+    Z, dY = rand(rows, cols, t, 1, mean=0.3, std=2.0), rand(rows, cols, t, 3)
+    dZ = rand(rows, cols, t, 4) if with_dz else None
+    w = rand(1, cols, t, 5, mean=1.0, std=0.3).view(-1)
+    _, mean, rstd = q.qlora_layernorm_fwd(Z, w)
+    dX, dR, dw, db = q.qlora_dropout_add_layernorm_bwd(dY, dZ, Z, mean, rstd, p, seed, offset, w)
+    z, dy, m, r, wv = f64(Z), f64(dY), f64(mean), f64(rstd), f64(w)
+    dx, ew, eb = layernorm_grads(dy, z, m, r, wv)
+    total = dx if dZ is None else dx + f64(dZ)
+    norm_err, bw, bb = bwd_bounds(dy, z, m, r, wv, dx, rows, cols, torch.float32)
+    err = norm_err + U * (np.abs(total) + norm_err)
+    check(dR, total, out_err(total, err, t), "dresidual")
+    dropped = dropout(total, p, seed, offset)
+    gain = 65536 / (65536 - round(65536 * p))
+    check(dX, dropped, out_err(dropped, gain * err + 2 * U * np.abs(dropped), t), "dX")
+    check(dw, ew, bw, "dweight")
+    check(db, eb, bb, "dbias")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,res", [(620, 8192, True), (620, 8192, False), (4877, 1000, True)])
+def test_dropout_of_many_groups(dtype, rows, cols, res):
+    """Sizes that take four groups of eight per thread, the last block in part."""
+    t = TYPES[dtype]
+    X, R = rand(rows, cols, t, 1), (rand(rows, cols, t, 2) if res else None)
+    Y = q.qlora_dropout_fwd(X, 0.3, 5, 9, residual=R)
+    ref = dropout(f64(X), 0.3, 5, 9, None if R is None else f64(R))
+    prod = np.abs(dropout(f64(X), 0.3, 5, 9))
+    check(Y, ref, out_err(ref, 2 * U * prod + U * np.abs(ref), t), "Y")
