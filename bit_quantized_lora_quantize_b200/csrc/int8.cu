@@ -9,19 +9,22 @@
 // enters in the epilogue.
 //
 // Three kernels:
-// - quantization: one pass, rows in registers, HBM-bound (4096 x 8192 in bf16
-//   20.4 us, 0.75 of the copy bandwidth; ragged, by scalar accesses, 4096 x 8191
-//   30.6 us);
+// - quantization: one pass, rows in registers (4096 x 8192 in bf16 20.3 us, 0.76
+//   of the copy bandwidth, with issue slots 71 % busy; ragged, by scalar
+//   accesses, 4096 x 8191 30.4 us);
 // - up to 16 tokens, bound by reading the weight: `token_kernel` streams it
 //   straight into the register fragments of mma.sync (one token, 8192 x 8192:
-//   15.6 us of which 10.3 are the weight at the copy bandwidth; four tokens,
-//   22016 x 8192: 34.9 us, 0.79 of it);
+//   16.2 us with the quantization, 10.3 are the weight at the copy bandwidth; four
+//   tokens, 22016 x 8192: 35.3 us, 0.78 of it).  Against the other kernel: 12
+//   tokens, 4096 x 4096 8.4 us and 16.5; 16 tokens, 8192 x 8192 23.2 and 23.0,
+//   22016 x 8192 56.7 and 50.9;
 // - more tokens: `pair_kernel`, CTA pairs (cta_group::2) with 256 x 256 tiles
 //   fed by a TMA ring; persistent, with two accumulators in TMEM so that a
 //   tile's epilogue runs under the next tile's products (4096 x 8192 x 8192:
-//   177 us, 3.1 P operations/s; tensor pipe 83 % busy), or, where the tiles
-//   fill less than half of the SMs, several pairs to a tile, each a part of
-//   the depth (300 x 11003 x 4099: 30.3 us).
+//   177 us, 3.1 P operations/s; tensor pipe 83 % busy; 196 us in a row of calls
+//   under the power cap), or, where the tiles fill less than half of the SMs,
+//   several pairs to a tile, each a part of the depth (300 x 11003 x 4099:
+//   30.3 us).
 //   Narrower tiles do not help: a tcgen05.mma over 128 rows per SM costs about
 //   the same for 16 columns as for 256 (8192 x 8192 with one token on that
 //   path: 24.8 us).
@@ -232,7 +235,9 @@ cudaError_t launch_quantize_rows(QuantArgs a, cudaStream_t stream) {
     return cudaGetLastError();
   }
   const bool vec = vector_rows(a.x, a.cols);
-  // Few rows: as many warps per row as its columns allow; else four steps each.
+  // Few rows: as many warps per row as its columns allow; else four steps each
+  // (bf16, 1 x 1024: 1.7 us, 2.1 with four; 290 x 4096: 2.6 against 2.7; at the
+  // rule's edge, 290 x 8192, 3.6 against 3.3).
   const int groups = a.rows <= 2 * device_sm_count() && a.cols <= 32 * 256 ? 1 : kQuantGroups;
   a.wpr = 1;
   while (static_cast<int64_t>(a.wpr) * 256 * groups < a.cols) a.wpr *= 2;

@@ -9,9 +9,9 @@
 //   dweight = sum over rows of dY h,  dbias = sum over rows of dY
 //   fused form: dresidual = dz, dX = dropout(dz) with the forward's draws
 //
-// All of it is HBM-bound: a row is read once into registers, the mean first
-// and then the squared distances from it (no difference of large sums), both
-// in float32.  The fused form takes the statistics of Z as rounded to its
+// HBM sets the floor of all of it: a row is read once into registers, the mean
+// first and then the squared distances from it (no difference of large sums),
+// both in float32.  The fused form takes the statistics of Z as rounded to its
 // type, which is what the backward pass reads.
 //
 // Forward: `wpr` warps share a row, 256 columns per warp and step, so that a
@@ -27,14 +27,18 @@
 // from run to run.  Rows of over 8192 columns take one block each and a second
 // pass for the parameters.
 //
-// Measured on 4096 x 8192, as a fraction of the copy bandwidth: forward 28.7 us
-// (0.71) in bf16 and 48.8 (0.84) in float32, fused 48.1 (0.85) and 95.4 (0.86);
-// backward 46.2 (0.66) and 68.6 (0.90), fused 70.9 (0.72) and 109 (0.94).  In
-// float32 HBM is the bound; in bf16 the instructions per element are (about 23
-// in the backward, 12 of them arithmetic on pairs, 6 unpacking), and the
-// forward's loads wait for the block's reductions before them.  Ragged rows take
-// scalar accesses: 777 x 5003 in fp16 8.7 us forward and 15.6 backward, against 6.6
-// and 14.1 of 777 x 5000.
+// Measured on 4096 x 8192, as a fraction of the copy bandwidth: forward 28.5 us
+// (0.72) in bf16 and 49.3 (0.83) in float32, fused 47.4 (0.86) and 96.0 (0.85);
+// backward 46.8 (0.66) and 68.3 (0.90), fused 70.9 (0.72) and 109 (0.94).  In
+// float32 HBM is the bound.  In bf16 latency is: the forward's loads wait for the
+// block's reductions before them, with nothing of the next row in flight; in the
+// backward 17 warps per SM, at 96 registers, wait for shared memory (each stage
+// is read and unpacked twice), for the ring and for one another, with issue
+// slots 49 %, the ALU 32 % and DRAM 46 % busy.  Ragged rows take scalar accesses:
+// 777 x 5003 in fp16 8.8 us forward and 15.8 backward, against 6.6 and 13.9 of
+// 777 x 5000.  Long rows: backward 166 us for 4096 x 11008 and 203 for
+// 4096 x 16384 in bf16, forward 141 for 4096 x 20480 (55 for 4096 x 16384, still
+// in registers).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -815,8 +819,10 @@ cudaError_t launch_fwd(LnFwdArgs a, const FwdDrop<FUSED>& drop, cudaStream_t str
     ln_fwd_long_kernel<T, W, kLong, FUSED><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a, drop);
     return cudaGetLastError();
   }
-  // Few rows: one step per warp where 32 warps allow it, for latency.
-  // Otherwise four steps, so that several rows share an SM.
+  // Few rows: one step per warp where 32 warps allow it, for latency (bf16,
+  // 1 x 8192: 3.0 us, 3.4 with four; 290 x 4096: 2.9 against 3.5; 290 x 8192, the
+  // rule's edge: 4.1 against 4.0).  Otherwise four steps, so that several rows
+  // share an SM.
   int groups = kFwdMaxGroups;
   if (a.rows <= 2 * device_sm_count() && a.cols <= 2 * kFwdWarps * 256) groups = 1;
   a.wpr = warps_for(a.cols, groups);
@@ -871,8 +877,11 @@ cudaError_t launch_bwd(LnBwdArgs a, bool vec, float* dw, float* db, cudaStream_t
   cudaError_t e;
   a.wpr = warps_for(std::min(a.cols, kBwdCols), kBwdGroups);
   const int slots = kBwdWarps / a.wpr;
-  // Rows a warp takes per step: two halve the fixed cost of a step, where
-  // their stages still leave three in the ring and there are steps enough.
+  // Rows a warp takes per step: two, where their stages still leave three in the
+  // ring and there are steps enough.  That pays for narrow and ragged rows (bf16,
+  // 32768 x 64: 15.4 us, 18.2 with one; 20000 x 250: 16.1 against 17.3;
+  // 4096 x 4095: 36.1 against 38.8) and costs a little for some wide aligned ones
+  // (4096 x 2048: 18.2 against 17.3; 4096 x 8192: 46.8 against 45.7).
   const auto plan = [&](int r) {
     // Room for a stage's rows at any alignment.
     const int64_t row_bytes = static_cast<int64_t>(std::min(a.cols, kBwdCols)) * sizeof(T);

@@ -264,9 +264,10 @@ __device__ __forceinline__ void store_cols(T* row, int c0, int cols, int lane, c
 // Philox4x32-10: Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
 // easy as 1, 2, 3" (SC 2011): ten rounds of two 32 x 32 -> 64 bit products
 // over a 128-bit counter, with a key that grows by a Weyl constant per round.
-// The integer pipe bounds every kernel that draws, so the rounds' keys come
-// from the host as constants (25.9 -> 20.9 us for 4096 x 8192 in bf16 together
-// with the comparison below).
+// The draws are most of what a drawing kernel issues (the dropout of 4096 x 8192
+// in bf16: ALU pipe 62 %, issue slots 61 % busy), so the rounds' keys come from
+// the host as constants (25.9 -> 20.9 us there, together with the comparison
+// below).
 struct Draws {
   uint32_t w[4];
 };

@@ -165,18 +165,20 @@ QLORA_API qlora_status qlora_dequantize_4bit(const uint8_t* codes, const uint8_t
  *                 bytes, filled with zeros once before its first use.  It
  *                 holds the status word read by qlora_check_status (first
  *                 256 bytes) and counters that every call leaves at zero;
- *                 everything else is overwritten before it is read.  Calls
- *                 that may overlap on the GPU need one each: results of calls
- *                 that share one are undefined, and where a GEMM of the large-M
- *                 calls finds another one at work, qlora_check_status reports
+ *                 everything else is overwritten before it is read.  The
+ *                 counters lie elsewhere for other sizes (M, K, N, r): fill it
+ *                 with zeros again before it serves those.  Calls that may
+ *                 overlap on the GPU need one each: results of calls that share
+ *                 one are undefined, and where a GEMM of the large-M calls
+ *                 finds another one at work, qlora_check_status reports
  *                 QLORA_ERR_OVERLAP.  After that or QLORA_ERR_TIMEOUT, fill it
  *                 with zeros again before the next call.
  * Supported: K % 64 == 0, N % 8 == 0 (the weight's blocks and the row
  * strides of Y, dY and B, which are copied by TMA, in 16-byte units),
  * 1 <= r <= 256, M, N, K < 2^31.  Otherwise QLORA_ERR_UNSUPPORTED.  Ranks
  * that are not multiples of 8 run with A, B, T_save, dA and dB padded with
- * zeros to the next multiple of 8 inside the workspace (a few small copy
- * kernels around the GEMM); ranks above 128 always take the pair GEMMs.
+ * zeros to the next multiple of 8 inside the workspace (a small copy kernel on
+ * either side of the GEMM); ranks above 128 always take the pair GEMMs.
  * For up to 8 tokens (up to 16 when N*K >= 2^27) the forward is two
  * launches chained by programmatic dependent launch: a weight stream that
  * also forms T, and a small kernel that sums its partials and adds T B;
