@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from .qlora import PackedNF4, QloraError, _check, lib, packed_sizes
+from .qlora import PackedNF4, QloraError, _check, lib, packed_sizes, qlora_workspace_bytes
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -283,7 +283,10 @@ def new_dropout_workspace(M: int, K: int, N: int, r: int, device) -> torch.Tenso
     nbytes = qlora_dropout_workspace_bytes(M, K, N, r)
     if nbytes == 0:
         raise QloraError("qlora_dropout_workspace_bytes", 3, f"M={M} K={K} N={N} r={r}")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    # what the plain calls keep; the rest, of M x K values, is written before it is read
+    ws[:qlora_workspace_bytes(M, K, N, r)].zero_()
+    return ws
 
 
 def _linear(X: torch.Tensor, W: PackedNF4, A: torch.Tensor, B: torch.Tensor, workspace: torch.Tensor | None):

@@ -341,8 +341,9 @@ QLORA_API qlora_status qlora_dropout_bwd(const void* dY, void* dX, int64_t rows,
  * Same supported shapes, code values, buffers and workspace rule as
  * qlora_linear_fwd_4bit / qlora_linear_bwd_4bit, with a workspace of at least
  * qlora_dropout_workspace_bytes bytes (during a call it holds a dropped copy of
- * X and, in float32, dY W', besides what the plain calls keep there).  Every M
- * runs the pair GEMMs of the large-M calls.  s * c must be finite
+ * X and, in float32, dY W', besides what the plain calls keep there; only that
+ * part, the first qlora_workspace_bytes bytes, needs the zeros).  Every M runs
+ * the pair GEMMs of the large-M calls.  s * c must be finite
  * (QLORA_ERR_INVALID_ARG), M * K at most 2^40.
  */
 QLORA_API qlora_status qlora_linear_fwd_dropout(const uint16_t* X, int64_t M, int64_t K, int64_t N,

@@ -191,3 +191,19 @@ def test_dx_is_rounded_once(M, K, N, r, p):
     eu = acc(N, a(dy) @ a(lb.T)) + (4 * U + H * H) * a(u)  # U's own sum, its scale and its bf16 pair
     err = acc(N, a(dy) @ a(w)) + gain * (eu @ a(la.T) + acc(2 * r, a(u) @ a(la.T))) + 4 * U * (a(add) + a(ref))
     check(dX, ref, err + H * (a(ref) + err), "dX")
+
+
+@pytest.mark.parametrize("M,r", [(16, 8), (140, 13)])
+def test_only_the_plain_part_of_the_workspace_needs_zeros(M, r):
+    """Whatever lies behind the plain calls' bytes (NaN here) changes nothing."""
+    case = synthetic.linear_case(M, 256, 264, r, 0.5, seed=5)
+    Wp = q.qlora_quantize_nf4(case.W.to(DEV))
+    X, A, B, dY = (t.to(DEV) for t in (case.X, case.A, case.B, case.dY))
+    got = []
+    for fill in (0, 255):
+        ws = q.new_dropout_workspace(M, 256, 264, r, DEV)
+        ws[q.qlora_workspace_bytes(M, 256, 264, r):].fill_(fill)
+        Y, T = q.qlora_linear_fwd_dropout(X, Wp, A, B, 0.5, 0.2, 3, workspace=ws)
+        got.append((Y, T, *q.qlora_linear_bwd_dropout(dY, X, T, Wp, A, B, 0.5, 0.2, 3, workspace=ws)))
+        assert q.qlora_check_status(ws) == 0
+    assert all(torch.equal(a, b) for a, b in zip(*got))
