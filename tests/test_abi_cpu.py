@@ -206,3 +206,8 @@ def test_product_path_has_no_cpu_fallback():
     import torch
     with pytest.raises(ValueError):
         q.qlora_quantize_nf4(torch.zeros(64, dtype=torch.bfloat16))
+
+
+def test_every_status_has_a_string_of_its_own(L):
+    names = [L.qlora_status_string(s) for s in range(8)]
+    assert len(set(names)) == 8 and b"unknown status" not in names and len(q.qlora.STATUS_NAMES) == 8
